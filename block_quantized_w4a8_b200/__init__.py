@@ -35,7 +35,8 @@ EXPORTS = ["w4a8_pack_q4_0", "w4a8_quant_act_q8_0", "w4a8_workspace_bytes", "w4a
            "w4a8_q4_k_backward_workspace_bytes", "w4a8_prepare_act",
            "w4a8_gemm_prepared", "w4a8_gemm_affine_prepared", "w4a8_gemm_noalloc", "w4a8_last_device_error",
            "w4a8_last_cuda_error_string", "w4a8_status_string", "w4a8_selftest_bounded_wait",
-           "w4a8_gemm_path"]
+           "w4a8_gemm_path", "w4a8_quant_act_fp8", "w4a8_pack_fp8", "w4a8_fp8_workspace_bytes", "w4a8_gemm_fp8",
+           "w4a8_gemm_fp8_backward"]
 KERNEL_NAMES = {1: "gemv", 2: "gemm_i8", 3: "gemm_tc", 4: "gemm_pair"}
 
 
@@ -78,6 +79,11 @@ SIGNATURES = {
     "w4a8_last_device_error": (_I, []),
     "w4a8_selftest_bounded_wait": (_I, [ctypes.c_ulonglong, _P, _P]),
     "w4a8_gemm_path": (_I, [_I, _I, _I, _I, _I]),
+    "w4a8_quant_act_fp8": (_I, [_P, _I, _I, _I, _P, _P, _P]),
+    "w4a8_pack_fp8": (_I, [_P, _I, _I, _I, _P, _P, _P]),
+    "w4a8_fp8_workspace_bytes": (_Z, [_I, _I, _I]),
+    "w4a8_gemm_fp8": (_I, [_I, _I, _I, _P, _I, _P, _P, _EPI, _P, _P, _Z, _P]),
+    "w4a8_gemm_fp8_backward": (_I, [_I, _I, _I, _P, _I, _P, _P, _I, _P, _P, _Z, _P]),
     "w4a8_status_string": (ctypes.c_char_p, [_I]),
     "w4a8_last_cuda_error_string": (ctypes.c_char_p, []),
 }
@@ -390,6 +396,73 @@ def w4a8_gemm_noalloc(x, qs, d, y, stream=None) -> None:
                                                                  _ptr(y, dev, M * N * 4, "y"), _stream(stream)))
 
 
+def _fp8_scales(N: int, K: int) -> int:
+    """Bytes of the 128 x 128 scales of an N x K FP8 weight."""
+    return -(-N // 128) * -(-K // 128) * 4
+
+
+def _element(t: torch.Tensor, name: str, *dtypes: torch.dtype) -> torch.Tensor:
+    if t.dtype not in dtypes:
+        raise ValueError(f"libw4a8: {name} is {t.dtype}; this call takes {' or '.join(map(str, dtypes))}")
+    return t
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def w4a8_quant_act_fp8(x, q, s, stream=None) -> None:
+    """x (M, K) f32 or bf16 -> e4m3 codes q (M, K) and f32 scales s (M, ceil(K/128))."""
+    M, K = x.shape
+    dev = _device(x)
+    _check("w4a8_quant_act_fp8",
+           load_library().w4a8_quant_act_fp8(_ptr(x, dev), _dtype(x), M, K,
+                                             _ptr(_element(q, "q", *_CODES), dev, M * K, "q"),
+                                             _ptr(_element(s, "s", torch.float32), dev, M * -(-K // 128) * 4, "s"),
+                                             _stream(stream)))
+
+
+def w4a8_pack_fp8(w, q, s, stream=None) -> None:
+    """w (N, K) f32 or bf16 -> e4m3 codes q (N, K) and f32 scales s (ceil(N/128), ceil(K/128))."""
+    N, K = w.shape
+    dev = _device(w)
+    _check("w4a8_pack_fp8",
+           load_library().w4a8_pack_fp8(_ptr(w, dev), _dtype(w), N, K,
+                                        _ptr(_element(q, "q", *_CODES), dev, N * K, "q"),
+                                        _ptr(_element(s, "s", torch.float32), dev, _fp8_scales(N, K), "s"),
+                                        _stream(stream)))
+
+
+def w4a8_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().w4a8_fp8_workspace_bytes(M, N, K))
+
+
+def w4a8_gemm_fp8(x, q, s, y, ws, bias=None, stream=None) -> None:
+    """y (M, N) f32 or bf16 = x (M, K) . W^T + bias, W in e4m3 (q, s from w4a8_pack_fp8)."""
+    M, K = x.shape
+    N = q.shape[0]
+    dev = _device(x)
+    epi = _epilogue(bias, y, N, dev)
+    _check("w4a8_gemm_fp8",
+           load_library().w4a8_gemm_fp8(M, N, K, _ptr(x, dev), _dtype(x),
+                                        _ptr(_element(q, "q", *_CODES), dev, N * K, "q"),
+                                        _ptr(_element(s, "s", torch.float32), dev, _fp8_scales(N, K), "s"),
+                                        ctypes.byref(epi), _ptr(y, dev, M * N * y.element_size(), "y"),
+                                        _ptr(ws, dev), ws.nbytes, _stream(stream)))
+
+
+def w4a8_gemm_fp8_backward(dy, q, s, dx, ws, stream=None) -> None:
+    """dx (M, K) f32 or bf16 = dy (M, N) . W (the input gradient), W in e4m3."""
+    M, N = dy.shape
+    K = dx.shape[1]
+    dev = _device(dy)
+    _check("w4a8_gemm_fp8_backward",
+           load_library().w4a8_gemm_fp8_backward(M, N, K, _ptr(dy, dev), _dtype(dy),
+                                                 _ptr(_element(q, "q", *_CODES), dev, N * K, "q"),
+                                                 _ptr(_element(s, "s", torch.float32), dev, _fp8_scales(N, K), "s"),
+                                                 _dtype(dx), _ptr(dx, dev, M * K * dx.element_size(), "dx"),
+                                                 _ptr(ws, dev), ws.nbytes, _stream(stream)))
+
+
 def w4a8_last_device_error() -> int:
     return int(load_library().w4a8_last_device_error())
 
@@ -490,3 +563,45 @@ def gemm_affine(x, q, s, b, group: int, path: int = PATH_AUTO, ws=None, stream=N
     ws = workspace(M, N, K, group, x.device) if ws is None else ws
     w4a8_gemm_affine_ex(x, q, s, b, y, ws, group, path, stream)
     return y
+
+
+def quant_act_fp8(x: torch.Tensor, stream=None):
+    M, K = x.shape
+    q = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=x.device)
+    s = torch.empty(M, -(-K // 128), dtype=torch.float32, device=x.device)
+    w4a8_quant_act_fp8(x, q, s, stream)
+    return q, s
+
+
+def pack_fp8(w: torch.Tensor, stream=None):
+    N, K = w.shape
+    q = torch.empty(N, K, dtype=torch.float8_e4m3fn, device=w.device)
+    s = torch.empty(-(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
+    w4a8_pack_fp8(w, q, s, stream)
+    return q, s
+
+
+def fp8_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    """Workspace of gemm_fp8 and gemm_fp8_backward for this shape."""
+    nbytes = w4a8_fp8_workspace_bytes(M, N, K)
+    if nbytes == 0:
+        raise W4A8Error("w4a8_fp8_workspace_bytes", 1)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def gemm_fp8(x, q, s, bias=None, out_dtype=torch.float32, ws=None, stream=None):
+    M, K = x.shape
+    N = q.shape[0]
+    y = torch.empty(M, N, dtype=out_dtype, device=x.device)
+    ws = fp8_workspace(M, N, K, x.device) if ws is None else ws
+    w4a8_gemm_fp8(x, q, s, y, ws, bias, stream)
+    return y
+
+
+def gemm_fp8_backward(dy, q, s, out_dtype=torch.float32, ws=None, stream=None):
+    M, N = dy.shape
+    K = q.shape[1]
+    dx = torch.empty(M, K, dtype=out_dtype, device=dy.device)
+    ws = fp8_workspace(M, N, K, dy.device) if ws is None else ws
+    w4a8_gemm_fp8_backward(dy, q, s, dx, ws, stream)
+    return dx

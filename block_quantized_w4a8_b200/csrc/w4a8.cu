@@ -1207,3 +1207,5 @@ const char* w4a8_status_string(w4a8_status s) {
 }
 
 }  // extern "C"
+
+#include "fp8_api.cuh"

@@ -308,6 +308,47 @@ w4a8_status w4a8_gemv_q4_k_backward(int M, int N, int K, const float* dy, const 
                                     void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * FP8 (e4m3) weights with one f32 scale per 128 x 128 tile, and activations quantised to
+ * e4m3 with one f32 scale per row and 128 columns. In both, per block:
+ *   s = max(amax / 448, 2^-126),  q = e4m3(x * (1/s))
+ * (448 is the largest e4m3 value; division, reciprocal and product in f32, each rounded to
+ * nearest; conversion to nearest, ties to even, saturating). amax ignores NaN. A NaN keeps the code
+ * 0x7F and an infinity makes its block's scale infinite, so every output that uses such a
+ * block is NaN (or infinite). Blocks at the right and lower edges hold what is left of the
+ * row or column. K must be a multiple of 16; N and M are free.
+ *  w4a8_quant_act_fp8 : x M x K (f32 or bf16) -> q M x K bytes, s M x ceil(K/128).
+ *  w4a8_pack_fp8      : w N x K (f32 or bf16) -> q N x K bytes, s ceil(N/128) x ceil(K/128).
+ * Errors: INVALID_ARG (null, sizes, K % 16), UNSUPPORTED (dtype), MISALIGNED, CUDA.
+ */
+w4a8_status w4a8_quant_act_fp8(const void* x, w4a8_dtype dtype, int M, int K, uint8_t* q, float* s,
+                               cudaStream_t stream);
+w4a8_status w4a8_pack_fp8(const void* w, w4a8_dtype dtype, int N, int K, uint8_t* q, float* s, cudaStream_t stream);
+
+/*
+ * The matmul on those weights and its input gradient.
+ *  w4a8_gemm_fp8          : y[m][n] = sum_b sx[m][b] * s[n/128][b] * sum_{k in b} qx[m][k] * q[n][k],
+ *                           x (M x K, f32 or bf16) quantised in the call as
+ *                           w4a8_quant_act_fp8 does; `epi` as in w4a8_gemm_epi (bias and
+ *                           output type, NULL: f32, no bias).
+ *  w4a8_gemm_fp8_backward : dx[m][k] = sum_b sd[m][b] * s[b][k/128] * sum_{n in b} qd[m][n] * q[n][k],
+ *                           dy (M x N, f32 or bf16) quantised in the call with one scale
+ *                           per row and 128 columns of N; dx M x K of dx_dtype. The weights
+ *                           are frozen codes and get no gradient.
+ * The products of two codes are exact; they are summed in f32. Every output is within
+ * 1e-5 * sum |terms| of the exact sum over the codes (plus the rounding to bf16).
+ * ws : w4a8_fp8_workspace_bytes(M, N, K) bytes (serves both calls; query it with the device
+ *      current), 16-byte aligned; contents ignored on entry, garbage afterwards. Calls that
+ *      share a workspace must be ordered on one stream. Returns 0 for invalid sizes.
+ * Errors: as w4a8_quant_act_fp8, plus WORKSPACE.
+ */
+size_t w4a8_fp8_workspace_bytes(int M, int N, int K);
+w4a8_status w4a8_gemm_fp8(int M, int N, int K, const void* x, w4a8_dtype dtype, const uint8_t* q, const float* s,
+                          const w4a8_epilogue* epi, void* y, void* ws, size_t ws_bytes, cudaStream_t stream);
+w4a8_status w4a8_gemm_fp8_backward(int M, int N, int K, const void* dy, w4a8_dtype dtype, const uint8_t* q,
+                                   const float* s, w4a8_dtype dx_dtype, void* dx, void* ws, size_t ws_bytes,
+                                   cudaStream_t stream);
+
+/*
  * w4a8_gemm for callers that cannot allocate device memory. Some callers are not allowed
  * to call cudaMalloc at all: a host application that reserves every byte of device memory
  * up front and owns its allocator, or a plug-in interface whose call signature carries

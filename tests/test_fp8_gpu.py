@@ -1,0 +1,194 @@
+"""The FP8 matmul on the GPU against its definition in 64 bits: codes and scales exact,
+outputs within 1e-5 * sum |terms| (the accumulation in f32) plus, for a bf16 output, half a
+step of the result (2^-8 relative, 2^-134 at the smallest)."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_w4a8_b200 as w4a8
+from tests import fp8_reference as ref
+
+pytestmark = pytest.mark.gpu
+TOL = 1e-5
+
+
+def rand(shape, seed, dtype=torch.float32, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g) * torch.exp(spread * torch.randn(shape[0], 1, generator=g))
+    return x.to(dtype)
+
+
+def check(y, yref, T, what=""):
+    got = y.float().cpu().numpy().astype(np.float64)
+    tol = TOL * T
+    if y.dtype == torch.bfloat16:
+        tol = tol * (1 + 2.0 ** -8) + np.abs(yref) * 2.0 ** -8 + 2.0 ** -134
+    err = np.abs(got - yref)
+    assert got.shape == yref.shape
+    assert np.all(err <= tol), f"{what}: {np.sum(err > tol)} of {err.size} outside, worst {np.max(err / np.maximum(T, 1e-300))}"
+
+
+def weights(N, K, seed):
+    w = rand((N, K), seed, spread=0.5)
+    q, s = w4a8.pack_fp8(w.cuda())
+    return q, s, ref.decode(q.view(torch.uint8).cpu().numpy()), s.cpu().numpy()
+
+
+# ------------------------------------------------------------------ quantisation
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 128), (3, 144), (5, 400), (130, 1936), (257, 4096)])
+def test_codes_and_scales_are_exact(M, K, dtype):
+    x = rand((M, K), M + K, dtype)
+    q, s = w4a8.quant_act_fp8(x.cuda())
+    rq, rs = ref.quant_rows(x.float().numpy())
+    assert np.array_equal(q.float().cpu().numpy(), rq) and np.array_equal(s.cpu().numpy(), rs)
+    q, s = w4a8.pack_fp8(x.cuda())
+    rq, rs = ref.pack(x.float().numpy())
+    assert np.array_equal(q.float().cpu().numpy(), rq) and np.array_equal(s.cpu().numpy(), rs)
+
+
+def test_special_values_in_the_codes():
+    x = torch.zeros(4, 256)
+    x[0, 3] = float("nan")
+    x[0, 4] = 2.0
+    x[1, 130] = float("inf")
+    x[1, 131] = 5.0
+    x[2, 0] = 1e-44
+    x[3, :] = torch.linspace(-3e38, 3e38, 256)
+    for fn, r in ((w4a8.quant_act_fp8, ref.quant_rows), (w4a8.pack_fp8, ref.pack)):
+        q, s = fn(x.cuda())
+        rq, rs = r(x.numpy())
+        assert np.array_equal(q.float().cpu().numpy(), rq, equal_nan=True)
+        assert np.array_equal(s.cpu().numpy(), rs)
+
+
+# ------------------------------------------------------------------ forward and gradient
+SHAPES = [(1, 1, 16), (1, 128, 128), (1, 4096, 4096), (2, 129, 144), (3, 200, 272), (8, 64, 4096), (16, 1000, 1040),
+          (17, 257, 512), (33, 130, 400), (64, 640, 1936), (65, 384, 256), (127, 127, 112), (128, 1536, 384),
+          (129, 256, 2048), (201, 1531, 1936), (256, 2048, 512), (300, 777, 4096), (1025, 520, 640)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gemm(M, N, K, dtype):
+    q, s, wq, ws = weights(N, K, N + K)
+    x = rand((M, K), M, dtype)
+    bias = torch.randn(N, generator=torch.Generator().manual_seed(1)) if N % 2 else None
+    y = w4a8.gemm_fp8(x.cuda(), q, s, bias=None if bias is None else bias.cuda(), out_dtype=dtype)
+    yref, T = ref.gemm(x.float().numpy(), wq, ws, None if bias is None else bias.numpy().astype(np.float64))
+    check(y, yref, T, f"{M}x{N}x{K}")
+    assert w4a8.w4a8_last_device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_backward(M, N, K, dtype):
+    q, s, wq, ws = weights(N, K, N + K + 1)
+    dy = rand((M, N), M + 1, dtype)
+    dx = w4a8.gemm_fp8_backward(dy.cuda(), q, s, out_dtype=dtype)
+    dref, T = ref.backward(dy.float().numpy(), wq, ws)
+    check(dx, dref, T, f"{M}x{N}x{K}")
+    assert w4a8.w4a8_last_device_error() == 0
+
+
+def test_backward_agrees_with_differences_of_the_forward():
+    """With x and dy on the e4m3 grid (scale 1 in every block, so neither call rounds its
+    input), <dy, y(x + e) - y(x - e)> = <dx, 2e> up to the f32 sums of both calls."""
+    M, N, K = 4, 256, 256
+    q, s, _, _ = weights(N, K, 5)
+    g = torch.Generator().manual_seed(2)
+    x = torch.randint(-7, 8, (M, K), generator=g).float() * 32
+    dy = torch.randint(-7, 8, (M, N), generator=g).float() * 32
+    x[:, ::128], dy[:, ::128] = 448.0, 448.0
+    e = torch.zeros(M, K)
+    e[:, 1::2] = 32.0  # steps of the grid: |x + e| <= 256, x + e is a code
+    x = x.cuda()
+    yp, ym = w4a8.gemm_fp8(x + e.cuda(), q, s).double(), w4a8.gemm_fp8(x - e.cuda(), q, s).double()
+    dx = w4a8.gemm_fp8_backward(dy.cuda(), q, s).double().cpu()
+    lhs = float((dy.double() * (yp - ym).cpu()).sum())
+    rhs = float((dx * 2 * e.double()).sum())
+    W = np.abs(ref.dequant(ref.decode(q.view(torch.uint8).cpu().numpy()), s.cpu().numpy()))
+    size = np.abs(dy.numpy()) @ W  # sum |terms| of dx
+    bound = 2 * TOL * float(np.sum(size * (2 * e.numpy() + 2 * (x.abs().cpu().numpy() + e.numpy()))))
+    assert abs(lhs - rhs) <= bound
+    assert bound < 0.05 * abs(rhs) + 0.05 * float(np.sum(size * 2 * e.numpy()))  # the bound says something
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_nan_and_infinity_reach_the_outputs_that_use_them_and_no_other(M):
+    N, K = 300, 512
+    q, s, _, _ = weights(N, K, 9)
+    x = rand((M, K), 3)
+    clean = w4a8.gemm_fp8(x.cuda(), q, s)
+    x[0, 5] = float("nan")
+    if M > 1:
+        x[M - 1, 200] = float("inf")
+    y = w4a8.gemm_fp8(x.cuda(), q, s)
+    assert torch.isnan(y[0]).all()
+    if M > 1:
+        assert not torch.isfinite(y[M - 1]).any()
+    if M > 2:
+        assert torch.equal(y[1:M - 1], clean[1:M - 1])
+
+
+@pytest.mark.parametrize("M", [1, 20, 200])
+def test_zero_rows_give_zero(M):
+    N, K = 130, 272
+    q, s, _, _ = weights(N, K, 11)
+    x = rand((M, K), 4)
+    x[M // 2] = 0
+    y = w4a8.gemm_fp8(x.cuda(), q, s, out_dtype=torch.bfloat16)
+    assert torch.equal(y[M // 2], torch.zeros_like(y[M // 2]))
+
+
+# ------------------------------------------------------------------ memory, streams, graphs
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 1040), (16, 129, 144), (70, 333, 400), (201, 1531, 1936)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_nothing_outside_the_outputs_is_written(M, N, K, dtype):
+    """Outputs and workspace sit between guard words, and every byte of the output is written."""
+    q, s, _, _ = weights(N, K, 13)
+    x, dy = rand((M, K), 1, dtype).cuda(), rand((M, N), 2, dtype).cuda()
+    need = w4a8.w4a8_fp8_workspace_bytes(M, N, K)
+    size = torch.empty(0, dtype=dtype).element_size()
+    for n, call in ((M * N, lambda o, w: w4a8.w4a8_gemm_fp8(x, q, s, o.view(M, N), w)),
+                    (M * K, lambda o, w: w4a8.w4a8_gemm_fp8_backward(dy, q, s, o.view(M, K), w))):
+        outs = []
+        for fill in (0x5A, 0xA5):
+            buf = torch.full((512 + n * size + 512,), fill, dtype=torch.uint8, device="cuda")
+            ws = torch.full((512 + need + 512,), fill, dtype=torch.uint8, device="cuda")
+            call(buf[512: 512 + n * size].view(dtype), ws[512: 512 + need])
+            torch.cuda.synchronize()
+            for b, inner in ((buf, n * size), (ws, need)):
+                assert torch.all(b[:512] == fill) and torch.all(b[512 + inner:] == fill)
+            outs.append(buf[512: 512 + n * size].clone())
+        assert torch.equal(outs[0], outs[1])  # also: the result does not depend on the workspace's contents
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (48, 512, 1024), (300, 512, 1024)])
+def test_side_streams_and_captured_graphs(M, N, K):
+    q, s, _, _ = weights(N, K, 17)
+    x, dy = rand((M, K), 1).cuda(), rand((M, N), 2).cuda()
+    y0, d0 = w4a8.gemm_fp8(x, q, s), w4a8.gemm_fp8_backward(dy, q, s)
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    ws = [w4a8.fp8_workspace(M, N, K) for _ in side]
+    out = []
+    for i, st in enumerate(side):  # two calls at once, each with a workspace of its own
+        with torch.cuda.stream(st):
+            out.append((w4a8.gemm_fp8(x, q, s, ws=ws[i]), w4a8.gemm_fp8_backward(dy, q, s, ws=ws[i])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, y0) and torch.equal(b, d0) for a, b in out)
+    y, dx = torch.empty_like(y0), torch.empty_like(d0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w4a8.w4a8_gemm_fp8(x, q, s, y, ws[0])
+        w4a8.w4a8_gemm_fp8_backward(dy, q, s, dx, ws[0])
+    for _ in range(3):
+        y.zero_(), dx.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, y0) and torch.equal(dx, d0)
+    x.copy_(rand((M, K), 7))  # the graph reads the new contents
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, w4a8.gemm_fp8(x, q, s))
