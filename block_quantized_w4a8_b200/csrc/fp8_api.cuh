@@ -42,8 +42,13 @@ w4a8_status run_fp8_quant(const void* x, w4a8_dtype dt, int M, int L, int pitch,
     return W4A8_OK;
 }
 
+// Token tile of the few-token kernel, and the pitch of the block-major scales: whole tiles
+// are copied, so the rows are padded to the largest tile a path may take (256 for CTA pairs).
+inline int fp8_token_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+inline int fp8_scale_pitch(int M) { return M <= 64 ? fp8_token_tile(M) : int(cdiv(M, 256) * 256); }
+
 // Workspace of a contraction over R columns: the quantised rows (codes of pitch
-// round_up(R, 16), block-major scales of pitch round_up(M, 4)).
+// round_up(R, 16), block-major scales).
 struct Fp8Ws {
     uint8_t* q;
     float* s;
@@ -55,7 +60,7 @@ Fp8Ws fp8_ws(void* ws, int M, int R) {
     char* base = static_cast<char*>(ws);
     size_t off = 0;
     w.pitch = int(cdiv(R, 16) * 16);
-    w.spitch = int(cdiv(M, 4) * 4);
+    w.spitch = fp8_scale_pitch(M);
     w.q = reinterpret_cast<uint8_t*>(base + off); off = align256(off + size_t(M) * w.pitch);
     w.s = reinterpret_cast<float*>(base + off); off = align256(off + size_t(w.spitch) * fp8_blocks(R) * 4);
     w.bytes = off;
@@ -63,6 +68,64 @@ Fp8Ws fp8_ws(void* ws, int M, int R) {
 }
 
 inline bool fp8_dims_ok(int M, int N, int K) { return dims_ok(M, N) && dims_ok(K, 1) && K % 16 == 0; }
+
+// CTA pairs on 256 x 256 tiles when they occupy at least half of the SMs; otherwise tiles of
+// 128 columns and at most 128 tokens, the contracted axis split over clusters.
+inline bool fp8_use_pair(int M, int C) { return M > 128 && cdiv(M, 256) * cdiv(C, 256) * 4 >= sm_count(); }
+
+template <int MN, bool TRANS>
+w4a8_status launch_fp8_rows(int M, int C, int R, const CUtensorMap& tw, const Fp8Ws& w, const float* s, int swcols,
+                            void* out, const Epilogue& epi, cudaStream_t stream) {
+    using G = fp8::RowsGeo<MN>;
+    const cudaError_t ea = smem_limit_once(fp8::gemm_rows_kernel<MN, TRANS>, G::SMEM);
+    if (ea != cudaSuccess) return cuda_status(ea);
+    CUtensorMap tx;
+    if (!encode_2d(&tx, w.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(R), uint64_t(M), uint64_t(w.pitch), 128, MN,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+        return W4A8_ERR_CUDA;
+    const int64_t tiles = cdiv(C, 128) * cdiv(M, MN);
+    const int nblk = fp8_blocks(R);
+    int64_t ks = int64_t(sm_count()) * G::CTAS / tiles;
+    if (ks > 8) ks = 8;
+    if (ks > nblk) ks = nblk;
+    if (ks < 1) ks = 1;
+    const int kbs = int(cdiv(nblk, ks));
+    ks = cdiv(nblk, kbs);  // every CTA has at least one block
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(ks), unsigned(cdiv(C, 128)), unsigned(cdiv(M, MN)));
+    cfg.blockDim = dim3(G::THREADS);
+    cfg.dynamicSmemBytes = G::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(ks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, fp8::gemm_rows_kernel<MN, TRANS>, M, C, R, tw, tx, (const float*)w.s,
+                                          w.spitch, s, swcols, kbs, out, epi));
+}
+
+template <bool TRANS>
+w4a8_status launch_fp8_pair(int M, int C, int R, const CUtensorMap& tw, const Fp8Ws& w, const float* s, int swcols,
+                            void* out, const Epilogue& epi, cudaStream_t stream) {
+    using G = fp8::PairGeo;
+    const cudaError_t ea = smem_limit_once(fp8::gemm_pair_fp8_kernel<TRANS>, G::SMEM);
+    if (ea != cudaSuccess) return cuda_status(ea);
+    CUtensorMap tx;
+    if (!encode_2d(&tx, w.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(R), uint64_t(M), uint64_t(w.pitch), 128, 128,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+        return W4A8_ERR_CUDA;
+    const int tm = int(cdiv(M, 256)), tc = int(cdiv(C, 256));
+    const int64_t tiles = int64_t(tm) * tc;
+    const int pairs = int(tiles < sm_count() / 2 ? tiles : sm_count() / 2);
+    return cuda_status(launch_pdl(fp8::gemm_pair_fp8_kernel<TRANS>, dim3(unsigned(2 * pairs)), dim3(G::THREADS),
+                                  size_t(G::SMEM), stream, M, C, R, tw, tx, (const float*)w.s, w.spitch, s, swcols, tm,
+                                  tc, out, epi));
+}
 
 // out (M x C) = in (M x R) . w, w = W^T (TRANS = false) or W (the input gradient).
 template <bool TRANS>
@@ -75,12 +138,21 @@ w4a8_status fp8_gemm_impl(int M, int N, int K, const void* in, w4a8_dtype dt, co
     const Fp8Ws w = fp8_ws(ws, M, R);
     if (!ws || ws_bytes < w.bytes) return W4A8_ERR_WORKSPACE;
     if (!aligned16(ws)) return W4A8_ERR_MISALIGNED;
-    w4a8_status st = run_fp8_quant(in, dt, M, R, w.pitch, w.q, w.s, 1, w.spitch, stream);
+    // one box = 128 x 128 codes, either way round
+    CUtensorMap tw;
+    if (!encode_2d(&tw, q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(K), uint64_t(N), uint64_t(K), 128, 128,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+        return W4A8_ERR_CUDA;
+    const w4a8_status st = run_fp8_quant(in, dt, M, R, w.pitch, w.q, w.s, 1, w.spitch, stream);
     if (st != W4A8_OK) return st;
-    const dim3 grid(unsigned(cdiv(M, 8)), unsigned(cdiv(C, 32)));
-    fp8::gemm_simple_kernel<TRANS><<<grid, 256, 0, stream>>>(M, C, R, w.q, w.pitch, w.s, 1, w.spitch, q, s,
-                                                            fp8_blocks(K), out, epi);
-    return launch_status();
+    const int swcols = fp8_blocks(K);
+    if (fp8_use_pair(M, C)) return launch_fp8_pair<TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
+    switch (fp8_token_tile(M)) {
+        case 16: return launch_fp8_rows<16, TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
+        case 32: return launch_fp8_rows<32, TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
+        case 64: return launch_fp8_rows<64, TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
+        default: return launch_fp8_rows<128, TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
+    }
 }
 
 }  // namespace

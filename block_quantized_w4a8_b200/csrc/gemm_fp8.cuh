@@ -1,37 +1,517 @@
 // FP8 (e4m3) matmul with 128-wide blocks: activations with one scale per row and block of
 // the contracted axis, weights with one scale per 128 x 128 tile.
+//
+//   out[m][c] = sum_b sa[b][m] * sw(b, c/128) * P_b[m][c],   P_b = sum_{r in b} a[m][r] * w(r, c)
+//
+// over blocks b of 128 of the contracted axis r. Forward: c = n, r = k, w(r, c) = q[c][r];
+// input gradient (TRANS): c = k, r = n, w(r, c) = q[r][c]. Each P_b is four
+// tcgen05.mma.kind::f8f6f4 of K = 32 into a fresh tensor-memory tile; the epilogue reads the
+// tile and adds it, times the two scales, to f32 accumulators in registers. Both weight
+// orders are read by the same TMA boxes of 128 x 128 bytes with the 128-byte swizzle: the
+// forward's box is a K-major operand, the gradient's the same bytes as an MN-major one.
 #pragma once
+
+#include <cuda.h>
 
 #include "fp8_quant.cuh"
 
 namespace w4a8 {
 namespace fp8 {
 
-__device__ __forceinline__ float decode(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+constexpr int kTile = 128 * 128;  // bytes of one operand tile
+
+// Shared-memory matrix descriptors with the 128-byte swizzle (atoms of 8 rows x 128 bytes,
+// 1024 bytes apart): for a K-major operand the 8-row groups follow one another along M/N,
+// for an MN-major one along K; one 128-byte row spans the whole K block, or the whole M/N
+// extent, so the other stride is never used.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
+    return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+           (uint64_t(2) << 61);
+}
+// Byte offset of the kk-th K = 32 slice inside a tile.
+template <bool MN_MAJOR>
+__device__ __forceinline__ uint32_t k_offset(int kk) {
+    return MN_MAJOR ? uint32_t(kk) * 32u * 128u : uint32_t(kk) * 32u;
+}
+// Instruction descriptor, kind::f8f6f4: A and B e4m3, D f32; ta / tb: operand is MN-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool ta, bool tb) {
+    return (1u << 4) | (ta ? 1u << 15 : 0u) | (tb ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void tmem_load(uint32_t t, uint32_t (&r)[16]) { tmem_ld_32x32_x16(t, r); }
+__device__ __forceinline__ void tmem_load(uint32_t t, uint32_t (&r)[32]) { tmem_ld_32x32(t, r); }
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) { tmem_wait_ld16(r); }
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) { tmem_wait_ld(r); }
+
+constexpr int kMaxStages = 8;
+constexpr int kMaxBufs = 8;
+
+// ------------------------------------------------------------------ few tokens
+// Weights on the MMA's 128 rows, MN tokens (16 to 128) as its columns: each weight tile is
+// read once per token tile. The blocks of the contracted axis are split over a cluster of up
+// to 8 CTAs, whose partial sums are added through distributed shared memory in a fixed order.
+template <int MN_>
+struct RowsGeo {
+    static constexpr int MN = MN_;
+    static constexpr int STAGE = kTile + MN * 128;
+    static constexpr int CTAS = MN <= 64 ? 2 : 1;             // CTAs per SM
+    static constexpr int NS = MN == 16 ? 6 : MN == 32 ? 5 : MN == 64 ? 4 : 6;
+    static constexpr int NBUF = MN <= 64 ? 4 : 4;             // tensor-memory tiles
+    static constexpr int COLS = MN * NBUF < 32 ? 32 : MN * NBUF;
+    static constexpr int CW = MN <= 64 ? MN : 64;             // columns per epilogue warp
+    static constexpr int EPI_WARPS = 4 * MN / CW;
+    static constexpr int LD = CW < 32 ? 16 : 32;
+    static constexpr int COPY_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1;
+    static constexpr int THREADS = (EPI_WARPS + 2) * 32;
+    static constexpr int OFF_SX = NS * STAGE;                 // token scales, one row per stage
+    static constexpr int OFF_CTRL = OFF_SX + NS * MN * 4;
+    static constexpr int SMEM = OFF_CTRL + 512 + 1024;
+    static_assert(128 * MN * 4 <= NS * STAGE, "partial sums fit the stages");
+    static_assert(NS <= kMaxStages && NBUF <= kMaxBufs && SMEM <= (CTAS == 2 ? 115712 : 232448), "shared memory");
+};
+struct RowsCtrl {
+    unsigned long long full[kMaxStages];   // TMA: 1 arrival + bytes
+    unsigned long long empty[kMaxStages];  // one arrival per epilogue warp
+    unsigned long long tfull[kMaxBufs];    // MMA commit
+    unsigned long long tempty[kMaxBufs];   // one arrival per epilogue warp
+    unsigned long long drain;
+    uint32_t tmem_base;
+    uint32_t abort;
+};
+static_assert(sizeof(RowsCtrl) <= 512, "control block");
+
+// Grid: x = split of the contracted axis (the cluster), y = 128-column tile, z = token tile.
+template <int MN, bool TRANS>
+__global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
+    gemm_rows_kernel(int M, int C, int R, const __grid_constant__ CUtensorMap tm_w,
+                     const __grid_constant__ CUtensorMap tm_x, const float* __restrict__ sx, int spitch,
+                     const float* __restrict__ sw, int swcols, int kbs, void* __restrict__ out, Epilogue epi) {
+    using G = RowsGeo<MN>;
+    constexpr int NS = G::NS, NBUF = G::NBUF, CW = G::CW, LD = G::LD;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    RowsCtrl* ctrl = reinterpret_cast<RowsCtrl*>(smem + G::OFF_CTRL);
+    float* ssx = reinterpret_cast<float*>(smem + G::OFF_SX);
+    volatile uint32_t* abort = &ctrl->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nblk = (R + kBlk - 1) / kBlk;
+    const int b0 = blockIdx.x * kbs;
+    const int Bl = min(nblk, b0 + kbs) - b0;  // at least 1 (host)
+    const int c0 = blockIdx.y * 128, m0 = blockIdx.z * MN;
+    auto bar = [](unsigned long long* p) { return smem_addr(p); };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(bar(&ctrl->full[s]), 1);
+            mbar_init(bar(&ctrl->empty[s]), G::EPI_WARPS);
+        }
+        for (int j = 0; j < NBUF; ++j) {
+            mbar_init(bar(&ctrl->tfull[j]), 1);
+            mbar_init(bar(&ctrl->tempty[j]), G::EPI_WARPS);
+        }
+        mbar_init(bar(&ctrl->drain), 1);
+        ctrl->abort = 0;
+        mbar_init_fence();
+    }
+    if (warp == G::MMA_WARP) {
+        tmem_alloc(smem_addr(&ctrl->tmem_base), G::COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = ctrl->tmem_base;
+    pdl_launch_dependents();
+    const uint32_t smem0 = smem_addr(smem);
+
+    float acc[CW];  // epilogue warps: this thread's output column (lane) for CW tokens
+    if (warp == G::COPY_WARP) {
+        const bool leader = elect_one();
+        auto load_w = [&](int it) {
+            const uint32_t fb = bar(&ctrl->full[it % NS]);
+            mbar_arrive_expect_tx(fb, uint32_t(G::STAGE + MN * 4));
+            const int r = (b0 + it) * kBlk;
+            tma_load_2d<1>(smem0 + (it % NS) * G::STAGE, &tm_w, TRANS ? c0 : r, TRANS ? r : c0, fb);
+        };
+        auto load_x = [&](int it) {
+            const uint32_t fb = bar(&ctrl->full[it % NS]);
+            tma_load_2d<1>(smem0 + (it % NS) * G::STAGE + kTile, &tm_x, (b0 + it) * kBlk, m0, fb);
+            bulk_g2s(smem_addr(ssx + (it % NS) * MN), sx + int64_t(b0 + it) * spitch + m0, MN * 4, fb);
+        };
+        // the weights do not depend on the preceding kernel (the activation's quantisation)
+        const int pre = min(NS, Bl);
+        if (leader)
+            for (int it = 0; it < pre; ++it) load_w(it);
+        pdl_wait_primary();
+        if (leader)
+            for (int it = 0; it < pre; ++it) load_x(it);
+        __syncwarp();
+        int issued = pre;
+        for (int it = pre; it < Bl; ++it) {
+            if (!bounded_wait_warp(bar(&ctrl->empty[it % NS]), ((it / NS) & 1) ^ 1, abort)) break;
+            if (leader) {
+                load_w(it);
+                load_x(it);
+            }
+            __syncwarp();
+            issued = it + 1;
+        }
+        for (int it = max(0, issued - NS); it < issued; ++it)
+            drain_wait_warp(bar(&ctrl->full[it % NS]), (it / NS) & 1, 200000ull);
+    } else if (warp == G::MMA_WARP) {
+        const bool leader = elect_one();
+        uint32_t local_abort = 0;
+        constexpr uint32_t idesc = idesc_e4m3(128, MN, TRANS, false);
+        for (int it = 0; it < Bl; ++it) {
+            const int slot = it % NS, buf = it % NBUF;
+            if (!bounded_wait_warp(bar(&ctrl->full[slot]), (it / NS) & 1, abort)) break;
+            if (!bounded_wait_warp(bar(&ctrl->tempty[buf]), ((it / NBUF) & 1) ^ 1, abort)) break;
+            tc_fence_after();
+            if (leader) {
+                const uint32_t w = smem0 + slot * G::STAGE, x = w + kTile;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f8(tmem_base + buf * MN, desc_sw128(w + k_offset<TRANS>(kk)), desc_sw128(x + k_offset<false>(kk)),
+                           idesc, kk != 0);
+                tc_commit(bar(&ctrl->tfull[buf]));
+            }
+            __syncwarp();
+        }
+        if (leader) tc_commit(bar(&ctrl->drain));
+        __syncwarp();
+        bounded_wait_warp(bar(&ctrl->drain), 0, &local_abort);
+    } else {
+        const int q = warp & 3, j0 = (warp >> 2) * CW;
+        const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16) + j0;
+#pragma unroll
+        for (int j = 0; j < CW; ++j) acc[j] = 0.0f;
+        const float* swp = TRANS ? sw + int64_t(b0) * swcols + blockIdx.y : sw + int64_t(blockIdx.y) * swcols + b0;
+        const int64_t swstep = TRANS ? swcols : 1;
+        float wnext = __ldg(swp);
+        for (int it = 0; it < Bl; ++it) {
+            const int slot = it % NS, buf = it % NBUF;
+            const float w = wnext;
+            if (it + 1 < Bl) wnext = __ldg(swp + (it + 1) * swstep);
+            if (!bounded_wait_warp(bar(&ctrl->tfull[buf]), (it / NBUF) & 1, abort)) break;
+            if (!bounded_wait_warp(bar(&ctrl->full[slot]), (it / NS) & 1, abort)) break;  // the scales' copy
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < CW; h += LD) {
+                uint32_t p[LD];
+                tmem_load(lane_base + buf * MN + h, p);
+                float s[LD];
+#pragma unroll
+                for (int j = 0; j < LD; j += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(ssx + slot * MN + j0 + h + j);
+                    s[j] = v.x; s[j + 1] = v.y; s[j + 2] = v.z; s[j + 3] = v.w;
+                }
+                tmem_wait(p);
+                if (h + LD == CW) {  // tile and scales are in registers
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_after(bar(&ctrl->empty[slot]), s[LD - 1]);
+                        mbar_arrive(bar(&ctrl->tempty[buf]));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < LD; ++j)
+                    acc[h + j] = fmaf(__uint_as_float(p[j]), __fmul_rn(w, s[j]), acc[h + j]);
+            }
+        }
+    }
+
+    const int ks = gridDim.x;
+    const int tokens = min(MN, M - m0);
+    if (ks > 1) {
+        // partial sums [token][128] over the stages, which every MMA has finished reading
+        float* red = reinterpret_cast<float*>(smem);
+        __syncthreads();
+        if (warp < G::EPI_WARPS) {
+            const int j0 = (warp >> 2) * CW;
+#pragma unroll
+            for (int j = 0; j < CW; ++j) red[(j0 + j) * 128 + (warp & 3) * 32 + lane] = acc[j];
+        }
+        cluster_sync();
+        if (!*abort) {
+            for (int i = blockIdx.x * 128 + threadIdx.x; threadIdx.x < 128 && i < tokens * 128; i += ks * 128) {
+                float v = 0.0f;
+                for (int z = 0; z < ks; ++z) v = __fadd_rn(v, ld_cluster(mapa_shared(smem0 + i * 4, z)));
+                const int c = c0 + (i & 127);
+                if (c < C) epi_store(out, int64_t(m0 + (i >> 7)) * C + c, c, v, epi);
+            }
+        }
+        cluster_sync();  // no CTA leaves while another reads its partial sums
+    } else if (warp < G::EPI_WARPS && !*abort) {
+        const int j0 = (warp >> 2) * CW, c = c0 + (warp & 3) * 32 + lane;
+        if (c < C) {
+#pragma unroll
+            for (int j = 0; j < CW; ++j)
+                if (j0 + j < tokens) epi_store(out, int64_t(m0 + j0 + j) * C + c, c, acc[j], epi);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == G::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, G::COLS);
+    }
 }
 
-// One thread per output: out[m][c] = sum_b sa[b][m] * sw * sum_{r in b} a[m][r] * w(r, c), the
-// contracted axis r of length R, output columns c < C. TRANS = false: w(r, c) = q[c * R + r]
-// (forward: C = N, R = K); true: q[r * C + c] (input gradient: C = K, R = N).
-template <bool TRANS>
-__global__ void __launch_bounds__(256) gemm_simple_kernel(int M, int C, int R, const uint8_t* __restrict__ a, int pitch,
-                                                          const float* __restrict__ sa, int64_t sarow, int64_t sablk,
-                                                          const uint8_t* __restrict__ q, const float* __restrict__ sw,
-                                                          int swcols, void* __restrict__ out, Epilogue epi) {
-    const int c = blockIdx.y * 32 + (threadIdx.x & 31);
-    const int m = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (c >= C || m >= M) return;
-    float acc = 0.0f;
-    for (int b = 0; b * kBlk < R; ++b) {
-        float p = 0.0f;
-        const int r1 = min(R, (b + 1) * kBlk);
-        for (int r = b * kBlk; r < r1; ++r)
-            p = fmaf(decode(a[int64_t(m) * pitch + r]), decode(TRANS ? q[int64_t(r) * C + c] : q[int64_t(c) * R + r]), p);
-        const float w = TRANS ? sw[int64_t(b) * swcols + c / kBlk] : sw[int64_t(c / kBlk) * swcols + b];
-        acc = fmaf(p, __fmul_rn(sa[m * sarow + b * sablk], w), acc);
+// ------------------------------------------------------------------ many tokens
+// CTA pairs (cta_group::2), persistent: tiles of 256 tokens x 256 output columns, each CTA
+// holding 128 tokens (its TMEM lanes) and staging half of the weight tile. Two tensor-memory
+// tiles of 256 columns alternate, so the MMAs of the next block run while the epilogue adds
+// the last one; the output of a tile is stored while the next tile's first blocks run.
+struct PairGeo {
+    static constexpr int STAGE = 2 * kTile;  // token tile, weight half
+    static constexpr int NS = 6;
+    static constexpr int NBUF = 2;
+    static constexpr int CW = 128;           // columns per epilogue warp
+    static constexpr int LD = 32;
+    static constexpr int EPI_WARPS = 8;
+    static constexpr int COPY_WARP = 8, MMA_WARP = 9;
+    static constexpr int THREADS = 320;
+    static constexpr int OFF_SX = NS * STAGE;
+    static constexpr int OFF_CTRL = OFF_SX + NS * 128 * 4;
+    static constexpr int SMEM = OFF_CTRL + 512 + 1024;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+struct PairCtrl {
+    unsigned long long full[kMaxStages];    // this CTA's copies (1 arrival + bytes)
+    unsigned long long empty[kMaxStages];   // one arrival per epilogue warp of this CTA
+    unsigned long long pfull[kMaxStages];   // even CTA: the odd CTA's stage is ready
+    unsigned long long tfull[2];            // pair commit, on both CTAs
+    unsigned long long tempty[2];           // even CTA: one arrival per epilogue warp of both
+    unsigned long long drain;
+    uint32_t tmem_base;
+    uint32_t abort;
+};
+static_assert(sizeof(PairCtrl) <= 512, "control block");
+
+// Tile order: token tiles fastest within bands of 16 column tiles, so that the CTAs running
+// at one time share weights and tokens in L2.
+__device__ __forceinline__ void pair_tile(int t, int tm, int tc, int& mt, int& ct) {
+    constexpr int BAND = 16;
+    const int band = t / (tm * BAND), in = t - band * tm * BAND;
+    const int w = min(BAND, tc - band * BAND);
+    mt = in / w;
+    ct = band * BAND + in - mt * w;
+}
+
+// y[row .. row+7] of columns n .. n+7 (row a multiple of 8 elements).
+__device__ __forceinline__ void epi_store8(void* y, int64_t idx, int n, const float* v, const Epilogue& e) {
+    if (e.out_bf16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(epi_value(e, n + 2 * i, v[2 * i]), epi_value(e, n + 2 * i + 1, v[2 * i + 1]));
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(y) + idx) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        epi_store4(y, idx, n, v[0], v[1], v[2], v[3], e);
+        epi_store4(y, idx + 4, n + 4, v[4], v[5], v[6], v[7], e);
     }
-    epi_store(out, int64_t(m) * C + c, c, acc, epi);
+}
+
+template <bool TRANS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
+    gemm_pair_fp8_kernel(int M, int C, int R, const __grid_constant__ CUtensorMap tm_w,
+                         const __grid_constant__ CUtensorMap tm_x, const float* __restrict__ sx, int spitch,
+                         const float* __restrict__ sw, int swcols, int tiles_m, int tiles_c, void* __restrict__ out,
+                         Epilogue epi) {
+    using G = PairGeo;
+    constexpr int NS = G::NS, NBUF = G::NBUF, CW = G::CW, LD = G::LD;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    PairCtrl* ctrl = reinterpret_cast<PairCtrl*>(smem + G::OFF_CTRL);
+    float* ssx = reinterpret_cast<float*>(smem + G::OFF_SX);
+    volatile uint32_t* abort = &ctrl->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int nblk = (R + kBlk - 1) / kBlk;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int ntiles = tiles_m * tiles_c;
+    auto bar = [](unsigned long long* p) { return smem_addr(p); };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(bar(&ctrl->full[s]), 1);
+            mbar_init(bar(&ctrl->empty[s]), G::EPI_WARPS);
+            mbar_init(bar(&ctrl->pfull[s]), 1);
+        }
+        for (int j = 0; j < NBUF; ++j) {
+            mbar_init(bar(&ctrl->tfull[j]), 1);
+            mbar_init(bar(&ctrl->tempty[j]), 2 * G::EPI_WARPS);
+        }
+        mbar_init(bar(&ctrl->drain), 1);
+        ctrl->abort = 0;
+        mbar_init_fence();
+    }
+    if (warp == G::MMA_WARP) {
+        tmem_alloc_pair(smem_addr(&ctrl->tmem_base), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated
+    tc_fence_after();
+    const uint32_t tmem_base = ctrl->tmem_base;
+    pdl_launch_dependents();
+    const uint32_t smem0 = smem_addr(smem);
+
+    if (warp == G::COPY_WARP) {
+        const bool leader = elect_one();
+        pdl_wait_primary();  // the token operand is written by the preceding kernel
+        int it = 0;
+        bool go = true;
+        for (int t = pair; t < ntiles && go; t += npairs) {
+            int mt, ct;
+            pair_tile(t, tiles_m, tiles_c, mt, ct);
+            const int m0 = mt * 256 + int(rank) * 128, c0 = ct * 256 + int(rank) * 128;
+            for (int b = 0; b < nblk; ++b, ++it) {
+                const int slot = it % NS;
+                if (!bounded_wait_warp(bar(&ctrl->empty[slot]), ((it / NS) & 1) ^ 1, abort)) {
+                    go = false;
+                    break;
+                }
+                if (leader) {
+                    const uint32_t fb = bar(&ctrl->full[slot]);
+                    mbar_arrive_expect_tx(fb, uint32_t(G::STAGE + 512));
+                    const uint32_t st = smem0 + slot * G::STAGE;
+                    tma_load_2d<1>(st, &tm_x, b * kBlk, m0, fb);
+                    tma_load_2d<1>(st + kTile, &tm_w, TRANS ? c0 : b * kBlk, TRANS ? b * kBlk : c0, fb);
+                    bulk_g2s(smem_addr(ssx + slot * 128), sx + int64_t(b) * spitch + m0, 512, fb);
+                }
+                __syncwarp();
+            }
+        }
+        for (int i = max(0, it - NS); i < it; ++i) drain_wait_warp(bar(&ctrl->full[i % NS]), (i / NS) & 1, 200000ull);
+    } else if (warp == G::MMA_WARP) {
+        const bool leader = elect_one();
+        uint32_t local_abort = 0;
+        int total = 0;  // blocks of all this pair's tiles
+        for (int t = pair; t < ntiles; t += npairs) total += nblk;
+        if (rank == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(256, 256, false, TRANS);
+            for (int it = 0; it < total; ++it) {
+                const int slot = it % NS, buf = it % NBUF;
+                if (!bounded_wait_warp(bar(&ctrl->full[slot]), (it / NS) & 1, abort)) break;
+                if (!bounded_wait_warp<true>(bar(&ctrl->pfull[slot]), (it / NS) & 1, abort)) break;
+                if (!bounded_wait_warp<true>(bar(&ctrl->tempty[buf]), ((it / NBUF) & 1) ^ 1, abort)) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t x = smem0 + slot * G::STAGE, w = x + kTile;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8_pair(tmem_base + buf * 256, desc_sw128(x + k_offset<false>(kk)),
+                                    desc_sw128(w + k_offset<TRANS>(kk)), idesc, kk != 0);
+                    tc_commit_pair(bar(&ctrl->tfull[buf]), 3);
+                }
+                __syncwarp();
+            }
+            if (leader) tc_commit_pair(bar(&ctrl->drain), 3);
+        } else {
+            const uint32_t pfull0 = mapa_shared(bar(&ctrl->pfull[0]), 0);
+            for (int it = 0; it < total; ++it) {
+                if (!bounded_wait_warp(bar(&ctrl->full[it % NS]), (it / NS) & 1, abort)) break;
+                if (leader) mbar_arrive_remote(pfull0 + uint32_t(it % NS) * 8u);
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+        bounded_wait_warp(bar(&ctrl->drain), 0, &local_abort);
+    } else {
+        const int q = warp & 3, half = warp >> 2;
+        const int r = q * 32 + lane;  // this thread's token within the CTA's 128
+        const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16) + half * CW;
+        const uint32_t tempty0 = rank == 0 ? bar(&ctrl->tempty[0]) : mapa_shared(bar(&ctrl->tempty[0]), 0);
+        float acc[CW];
+        int it = 0;
+        bool go = true;
+        for (int t = pair; t < ntiles && go; t += npairs) {
+            int mt, ct;
+            pair_tile(t, tiles_m, tiles_c, mt, ct);
+            const int cb = ct * 2 + half;  // weight scale column of this warp
+            const bool inside = cb * 128 < C;
+            const float* swp = TRANS ? sw + cb : sw + int64_t(cb) * swcols;
+            const int64_t swstep = TRANS ? swcols : 1;
+#pragma unroll
+            for (int j = 0; j < CW; ++j) acc[j] = 0.0f;
+            float wnext = inside ? __ldg(swp) : 0.0f;
+            for (int b = 0; b < nblk; ++b, ++it) {
+                const int slot = it % NS, buf = it % NBUF;
+                const float w = wnext;
+                if (inside && b + 1 < nblk) wnext = __ldg(swp + (b + 1) * swstep);
+                if (!bounded_wait_warp<true>(bar(&ctrl->tfull[buf]), (it / NBUF) & 1, abort) ||
+                    !bounded_wait_warp(bar(&ctrl->full[slot]), (it / NS) & 1, abort)) {  // the scales' copy
+                    go = false;
+                    break;
+                }
+                tc_fence_after();
+                const float s = ssx[slot * 128 + r];
+                __syncwarp();
+                if (lane == 0) mbar_arrive_after(bar(&ctrl->empty[slot]), s);
+                const float f = __fmul_rn(s, w);
+#pragma unroll
+                for (int h = 0; h < CW; h += LD) {
+                    uint32_t p[LD];
+                    tmem_load(lane_base + buf * 256 + h, p);
+                    tmem_wait(p);
+                    if (h + LD == CW) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (rank == 0)
+                                mbar_arrive(tempty0 + uint32_t(buf) * 8u);
+                            else
+                                mbar_arrive_remote(tempty0 + uint32_t(buf) * 8u);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < LD; ++j) acc[h + j] = fmaf(__uint_as_float(p[j]), f, acc[h + j]);
+                }
+            }
+            const int m = mt * 256 + int(rank) * 128 + r, c = cb * 128;
+            if (go && inside && m < M) {
+                const int64_t row = int64_t(m) * C;
+                if ((C & 7) == 0 && c + CW <= C) {
+#pragma unroll
+                    for (int j = 0; j < CW; j += 8) epi_store8(out, row + c + j, c + j, acc + j, epi);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < CW; ++j)
+                        if (c + j < C) epi_store(out, row + c + j, c + j, acc[j], epi);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    cluster_sync();
+    if (warp == G::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
 }
 
 }  // namespace fp8

@@ -65,7 +65,9 @@ def test_special_values_in_the_codes():
 # ------------------------------------------------------------------ forward and gradient
 SHAPES = [(1, 1, 16), (1, 128, 128), (1, 4096, 4096), (2, 129, 144), (3, 200, 272), (8, 64, 4096), (16, 1000, 1040),
           (17, 257, 512), (33, 130, 400), (64, 640, 1936), (65, 384, 256), (127, 127, 112), (128, 1536, 384),
-          (129, 256, 2048), (201, 1531, 1936), (256, 2048, 512), (300, 777, 4096), (1025, 520, 640)]
+          (129, 256, 2048), (201, 1531, 1936), (256, 2048, 512), (300, 777, 4096), (1025, 520, 640),
+          # whole grids of 256 x 256 tiles (CTA pairs) in both directions, ragged and even
+          (1025, 2100, 2064), (2500, 1024, 1040), (2048, 1280, 1280), (513, 3333, 4000)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -114,7 +116,7 @@ def test_backward_agrees_with_differences_of_the_forward():
     assert bound < 0.05 * abs(rhs) + 0.05 * float(np.sum(size * 2 * e.numpy()))  # the bound says something
 
 
-@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("M", [1, 40, 300, 5000])
 def test_nan_and_infinity_reach_the_outputs_that_use_them_and_no_other(M):
     N, K = 300, 512
     q, s, _, _ = weights(N, K, 9)
@@ -142,7 +144,8 @@ def test_zero_rows_give_zero(M):
 
 
 # ------------------------------------------------------------------ memory, streams, graphs
-@pytest.mark.parametrize("M,N,K", [(1, 1000, 1040), (16, 129, 144), (70, 333, 400), (201, 1531, 1936)])
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 1040), (16, 129, 144), (70, 333, 400), (201, 1531, 1936),
+                                   (1100, 2090, 2064)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_nothing_outside_the_outputs_is_written(M, N, K, dtype):
     """Outputs and workspace sit between guard words, and every byte of the output is written."""
@@ -164,7 +167,7 @@ def test_nothing_outside_the_outputs_is_written(M, N, K, dtype):
         assert torch.equal(outs[0], outs[1])  # also: the result does not depend on the workspace's contents
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (48, 512, 1024), (300, 512, 1024)])
+@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (48, 512, 1024), (300, 512, 1024), (2560, 1024, 1024)])
 def test_side_streams_and_captured_graphs(M, N, K):
     q, s, _, _ = weights(N, K, 17)
     x, dy = rand((M, K), 1).cuda(), rand((M, N), 2).cuda()
