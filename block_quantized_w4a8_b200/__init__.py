@@ -36,7 +36,8 @@ EXPORTS = ["w4a8_pack_q4_0", "w4a8_quant_act_q8_0", "w4a8_workspace_bytes", "w4a
            "w4a8_gemm_prepared", "w4a8_gemm_affine_prepared", "w4a8_gemm_noalloc", "w4a8_last_device_error",
            "w4a8_last_cuda_error_string", "w4a8_status_string", "w4a8_selftest_bounded_wait",
            "w4a8_gemm_path", "w4a8_quant_act_fp8", "w4a8_pack_fp8", "w4a8_fp8_workspace_bytes", "w4a8_gemm_fp8",
-           "w4a8_gemm_fp8_backward"]
+           "w4a8_gemm_fp8_backward", "w4a8_moe_route", "w4a8_moe_workspace_bytes", "w4a8_moe_q4_0",
+           "w4a8_moe_layer_q4_0"]
 KERNEL_NAMES = {1: "gemv", 2: "gemm_i8", 3: "gemm_tc", 4: "gemm_pair"}
 
 
@@ -84,6 +85,11 @@ SIGNATURES = {
     "w4a8_fp8_workspace_bytes": (_Z, [_I, _I, _I]),
     "w4a8_gemm_fp8": (_I, [_I, _I, _I, _P, _I, _P, _P, _EPI, _P, _P, _Z, _P]),
     "w4a8_gemm_fp8_backward": (_I, [_I, _I, _I, _P, _I, _P, _P, _I, _P, _P, _Z, _P]),
+    "w4a8_moe_route": (_I, [_I, _I, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P]),
+    "w4a8_moe_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
+    "w4a8_moe_q4_0": (_I, [_I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P, _Z, _P]),
+    "w4a8_moe_layer_q4_0": (_I, [_I, _I, _I, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P, _Z,
+                                 _P]),
     "w4a8_status_string": (ctypes.c_char_p, [_I]),
     "w4a8_last_cuda_error_string": (ctypes.c_char_p, []),
 }
@@ -463,6 +469,65 @@ def w4a8_gemm_fp8_backward(dy, q, s, dx, ws, stream=None) -> None:
                                                  _ptr(ws, dev), ws.nbytes, _stream(stream)))
 
 
+def w4a8_moe_route(x, wr, top_k: int, ids, weights, renorm: bool = True, stream=None) -> None:
+    """Softmax top-k router: x (T, H), wr (E, H) -> ids (T, top_k) int32, weights (T, top_k) f32."""
+    T, H = x.shape
+    E = wr.shape[0]
+    dev = _device(x)
+    n = T * top_k * 4
+    _check("w4a8_moe_route",
+           load_library().w4a8_moe_route(T, E, H, top_k, int(renorm), _ptr(x, dev), _dtype(x),
+                                         _ptr(wr, dev, E * H * wr.element_size(), "wr"), _dtype(wr),
+                                         _ptr(_element(ids, "ids", torch.int32), dev, n, "ids"),
+                                         _ptr(_element(weights, "weights", torch.float32), dev, n, "weights"),
+                                         _stream(stream)))
+
+
+def w4a8_moe_workspace_bytes(T: int, E: int, H: int, I: int, top_k: int) -> int:
+    return int(load_library().w4a8_moe_workspace_bytes(T, E, H, I, top_k))
+
+
+def _experts(dev: int, H: int, gu_qs, gu_d, dn_qs, dn_d):
+    """(E, I) and the pointers of stacked experts: gu_qs (E, 2I, H/2), gu_d (E, 2I, H/32),
+    dn_qs (E, H, I/2), dn_d (E, H, I/32)."""
+    E, I = gu_qs.shape[0], gu_qs.shape[1] // 2
+    gq, gd = _q4_0_bytes(E * 2 * I, H)
+    dq, dd = _q4_0_bytes(E * H, I)
+    return E, I, (_ptr(gu_qs, dev, gq, "gu_qs"), _ptr(gu_d, dev, gd, "gu_d"), _ptr(dn_qs, dev, dq, "dn_qs"),
+                  _ptr(dn_d, dev, dd, "dn_d"))
+
+
+def w4a8_moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, y, ws, stream=None) -> None:
+    """y (T, H) f32 or bf16 = sum over a token's slots of weights * expert(ids); ids (T, top_k)."""
+    T, H = x.shape
+    top_k = ids.shape[1]
+    dev = _device(x)
+    E, I, experts = _experts(dev, H, gu_qs, gu_d, dn_qs, dn_d)
+    n = T * top_k * 4
+    _check("w4a8_moe_q4_0",
+           load_library().w4a8_moe_q4_0(T, E, H, I, top_k, _ptr(x, dev), _dtype(x),
+                                        _ptr(_element(ids, "ids", torch.int32), dev, n, "ids"),
+                                        _ptr(_element(weights, "weights", torch.float32), dev, n, "weights"), *experts,
+                                        _dtype(y), _ptr(y, dev, T * H * y.element_size(), "y"), _ptr(ws, dev),
+                                        ws.nbytes, _stream(stream)))
+
+
+def w4a8_moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k: int, ids, weights, y, ws, renorm: bool = True,
+                        stream=None) -> None:
+    """Router and experts in one call; writes ids, weights (T, top_k) and y (T, H)."""
+    T, H = x.shape
+    dev = _device(x)
+    E, I, experts = _experts(dev, H, gu_qs, gu_d, dn_qs, dn_d)
+    n = T * top_k * 4
+    _check("w4a8_moe_layer_q4_0",
+           load_library().w4a8_moe_layer_q4_0(T, E, H, I, top_k, int(renorm), _ptr(x, dev), _dtype(x),
+                                              _ptr(wr, dev, E * H * wr.element_size(), "wr"), _dtype(wr), *experts,
+                                              _ptr(_element(ids, "ids", torch.int32), dev, n, "ids"),
+                                              _ptr(_element(weights, "weights", torch.float32), dev, n, "weights"),
+                                              _dtype(y), _ptr(y, dev, T * H * y.element_size(), "y"), _ptr(ws, dev),
+                                              ws.nbytes, _stream(stream)))
+
+
 def w4a8_last_device_error() -> int:
     return int(load_library().w4a8_last_device_error())
 
@@ -605,3 +670,40 @@ def gemm_fp8_backward(dy, q, s, out_dtype=torch.float32, ws=None, stream=None):
     ws = fp8_workspace(M, N, K, dy.device) if ws is None else ws
     w4a8_gemm_fp8_backward(dy, q, s, dx, ws, stream)
     return dx
+
+
+def moe_route(x, wr, top_k: int, renorm: bool = True, stream=None):
+    ids = torch.empty(x.shape[0], top_k, dtype=torch.int32, device=x.device)
+    weights = torch.empty(x.shape[0], top_k, dtype=torch.float32, device=x.device)
+    w4a8_moe_route(x, wr, top_k, ids, weights, renorm, stream)
+    return ids, weights
+
+
+def moe_workspace(T: int, E: int, H: int, I: int, top_k: int, device="cuda") -> torch.Tensor:
+    """Workspace of moe_q4_0 and moe_layer_q4_0 for this shape."""
+    nbytes = w4a8_moe_workspace_bytes(T, E, H, I, top_k)
+    if nbytes == 0:
+        raise W4A8Error("w4a8_moe_workspace_bytes", 1)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, out_dtype=torch.float32, ws=None, stream=None):
+    T, H = x.shape
+    y = torch.empty(T, H, dtype=out_dtype, device=x.device)
+    if ws is None:
+        ws = moe_workspace(T, gu_qs.shape[0], H, gu_qs.shape[1] // 2, ids.shape[1], x.device)
+    w4a8_moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, y, ws, stream)
+    return y
+
+
+def moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k: int, renorm: bool = True, out_dtype=torch.float32, ws=None,
+                   stream=None):
+    """(y, ids, weights) of the routed layer."""
+    T, H = x.shape
+    ids = torch.empty(T, top_k, dtype=torch.int32, device=x.device)
+    weights = torch.empty(T, top_k, dtype=torch.float32, device=x.device)
+    y = torch.empty(T, H, dtype=out_dtype, device=x.device)
+    if ws is None:
+        ws = moe_workspace(T, gu_qs.shape[0], H, gu_qs.shape[1] // 2, top_k, x.device)
+    w4a8_moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k, ids, weights, y, ws, renorm, stream)
+    return y, ids, weights

@@ -1209,3 +1209,4 @@ const char* w4a8_status_string(w4a8_status s) {
 }  // extern "C"
 
 #include "fp8_api.cuh"
+#include "moe_api.cuh"

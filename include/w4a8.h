@@ -349,6 +349,51 @@ w4a8_status w4a8_gemm_fp8_backward(int M, int N, int K, const void* dy, w4a8_dty
                                    cudaStream_t stream);
 
 /*
+ * Mixture-of-experts layer for a few tokens, Q4_0 experts with Q8_0 activations.
+ *
+ *  w4a8_moe_route      : logits l = x . Wr^T (x T x H, Wr E x H, each f32 or bf16; f32 sums), the
+ *                        top_k largest per token in falling order (the lower index on
+ *                        ties; a NaN ranks below every number), and their weights
+ *                        p = softmax of the logits over the chosen experts (renorm != 0) or
+ *                        over all E (renorm = 0). ids T x top_k int32, weights T x top_k f32.
+ *                        T up to W4A8_MAX_DIM.
+ *  w4a8_moe_q4_0       : y[t] = sum_s weights[t][s] * down(e), e = ids[t][s], with
+ *                          g = xq . Wg[e]^T, u = xq . Wu[e]^T   (as w4a8_gemm, xq = Q8_0(x[t]))
+ *                          h = g / (1 + exp(-g)) * u            (f32)
+ *                          down(e) = hq . Wd[e]^T               (hq = Q8_0(h))
+ *                        A slot whose id is negative or not below E is empty and adds
+ *                        nothing (a token with only empty slots gets a row of zeros); an
+ *                        expert named by two slots of a token counts with the sum of their weights.
+ *  w4a8_moe_layer_q4_0 : both; writes ids and weights too.
+ *
+ * gu_qs, gu_d : w4a8_pack_q4_0 of the E x 2I rows of H: per expert I gate rows, then I up rows.
+ * dn_qs, dn_d : w4a8_pack_q4_0 of the E x H rows of I.
+ * y           : T x H of out_dtype (f32, or bf16 rounded once).
+ * ws          : w4a8_moe_workspace_bytes bytes, 16-byte aligned; contents ignored on entry,
+ *               garbage afterwards. Calls that share one must be ordered on one stream.
+ *               Returns 0 for sizes the calls refuse.
+ * Limits: T <= W4A8_MOE_MAX_TOKENS (the routed calls), E <= W4A8_MOE_MAX_EXPERTS, top_k <=
+ * min(E, W4A8_MOE_MAX_TOPK), I <= W4A8_MAX_DIM / 2; H and I multiples of 32.
+ * Errors: INVALID_ARG (null, sizes), UNSUPPORTED (a limit, a dtype), MISALIGNED, WORKSPACE, CUDA.
+ */
+#define W4A8_MOE_MAX_TOKENS 64
+#define W4A8_MOE_MAX_EXPERTS 256
+#define W4A8_MOE_MAX_TOPK 16
+w4a8_status w4a8_moe_route(int T, int E, int H, int top_k, int renorm, const void* x, w4a8_dtype dtype,
+                           const void* wr, w4a8_dtype wr_dtype, int32_t* ids, float* weights,
+                           cudaStream_t stream);
+size_t w4a8_moe_workspace_bytes(int T, int E, int H, int I, int top_k);
+w4a8_status w4a8_moe_q4_0(int T, int E, int H, int I, int top_k, const void* x, w4a8_dtype dtype,
+                          const int32_t* ids, const float* weights, const uint8_t* gu_qs, const uint16_t* gu_d,
+                          const uint8_t* dn_qs, const uint16_t* dn_d, w4a8_dtype out_dtype, void* y, void* ws,
+                          size_t ws_bytes, cudaStream_t stream);
+w4a8_status w4a8_moe_layer_q4_0(int T, int E, int H, int I, int top_k, int renorm, const void* x,
+                                w4a8_dtype dtype, const void* wr, w4a8_dtype wr_dtype, const uint8_t* gu_qs,
+                                const uint16_t* gu_d, const uint8_t* dn_qs, const uint16_t* dn_d, int32_t* ids,
+                                float* weights, w4a8_dtype out_dtype, void* y, void* ws, size_t ws_bytes,
+                                cudaStream_t stream);
+
+/*
  * w4a8_gemm for callers that cannot allocate device memory. Some callers are not allowed
  * to call cudaMalloc at all: a host application that reserves every byte of device memory
  * up front and owns its allocator, or a plug-in interface whose call signature carries

@@ -1,0 +1,157 @@
+"""Host side of the mixture-of-experts layer (no GPU): the reference the GPU tests use,
+refusals with the documented status codes, workspace sizes, and the binding's checks."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_w4a8_b200 as w4a8
+import oracle
+from tests import moe_reference as ref
+from tests.test_binding import fake  # noqa: F401  (the stand-in library)
+
+FAKE = 0x10000
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from block_quantized_w4a8_b200 import build
+    build.build()
+    return w4a8.load_library()
+
+
+# ------------------------------------------------------------------ the reference
+def test_reference_codes_are_the_oracles():
+    rng = np.random.default_rng(3)
+    w = rng.standard_normal((5, 96)).astype(np.float32)
+    qs, d = oracle.pack_q4_0(w)
+    assert np.array_equal(ref.dequant_q4_0(qs, d), oracle.dequant_q4_0(qs, d))
+    q, dx, _ = oracle.quant_act_q8_0(w)
+    codes, scales = ref.q8_0(w)
+    assert np.array_equal(codes.reshape(5, 96), q) and np.array_equal(scales, dx)
+
+
+def test_reference_route_breaks_ties_by_the_lower_index():
+    x = np.ones((1, 32))
+    wr = np.zeros((6, 32))
+    wr[2], wr[4], wr[5] = 1, 1, 2
+    ids, p, _ = ref.route(x, wr, 4, True)
+    assert ids.tolist() == [[5, 2, 4, 0]] and abs(p.sum() - 1) < 1e-15
+
+
+def test_reference_layer_is_the_plain_formula_up_to_its_bound():
+    """Against h kept in 64 bits: the difference is at most half a code step per element."""
+    rng = np.random.default_rng(4)
+    T, E, H, I = 3, 4, 64, 96
+    x = rng.standard_normal((T, H)).astype(np.float32)
+    gu, dn = rng.standard_normal((E, 2 * I, H)), rng.standard_normal((E, H, I))
+    ids = np.array([[0, 3], [1, -1], [9, -5]])
+    w = rng.random((T, 2))
+    y, bound = ref.experts(x, ids, w, gu, dn, 0.0)
+    xv = ref.values(*ref.q8_0(x))
+    assert np.all(y[2] == 0)
+    for t in range(2):
+        want, slack = np.zeros(H), np.zeros(H)
+        for s in range(2):
+            if ids[t, s] < 0:
+                continue
+            a = gu[ids[t, s]] @ xv[t]
+            h = a[:I] / (1 + np.exp(-a[:I])) * a[I:]
+            step = np.repeat(np.abs(h).reshape(-1, 32).max(1) / 127, 32)
+            want += w[t, s] * dn[ids[t, s]] @ h
+            slack += w[t, s] * np.abs(dn[ids[t, s]]) @ (step / 2)
+        assert np.all(np.abs(y[t] - want) <= slack * (1 + 1e-6) + bound[t])
+    assert np.all(bound < 1e-3 * np.abs(y).max() + 1e-9)  # with exact dots almost nothing may flip
+
+
+# ------------------------------------------------------------------ the C ABI's refusals
+def _route(lib, T=4, E=8, H=64, k=2, x=FAKE, dt=0, wr=FAKE, wdt=0, ids=FAKE, w=FAKE):
+    return lib.w4a8_moe_route(T, E, H, k, 1, P(x), dt, P(wr), wdt, P(ids), P(w), P(0))
+
+
+def _moe(lib, T=4, E=8, H=64, I=96, k=2, x=FAKE, dt=0, ids=FAKE, w=FAKE, gq=FAKE, gd=FAKE, dq=FAKE, dd=FAKE, odt=0,
+         y=FAKE, ws=FAKE, wsb=1 << 40):
+    return lib.w4a8_moe_q4_0(T, E, H, I, k, P(x), dt, P(ids), P(w), P(gq), P(gd), P(dq), P(dd), odt, P(y), P(ws), wsb,
+                             P(0))
+
+
+def _layer(lib, T=4, E=8, H=64, I=96, k=2, x=FAKE, dt=0, wr=FAKE, wdt=0, ids=FAKE, w=FAKE, gq=FAKE, gd=FAKE, dq=FAKE,
+           dd=FAKE, odt=0, y=FAKE, ws=FAKE, wsb=1 << 40):
+    return lib.w4a8_moe_layer_q4_0(T, E, H, I, k, 1, P(x), dt, P(wr), wdt, P(gq), P(gd), P(dq), P(dd), P(ids), P(w),
+                                   odt, P(y), P(ws), wsb, P(0))
+
+
+@pytest.mark.parametrize("call", [_route, _moe, _layer])
+def test_argument_errors(lib, call):
+    assert call(lib, T=0) == 1 and call(lib, E=0) == 1 and call(lib, k=0) == 1 and call(lib, H=-32) == 1
+    assert call(lib, H=48) == 1 and call(lib, H=1 << 21) == 1
+    assert call(lib, x=0) == 1 and call(lib, ids=0) == 1 and call(lib, w=0) == 1
+    assert call(lib, dt=7) == 2 and call(lib, E=257) == 2 and call(lib, k=9) == 2 and call(lib, E=64, k=17) == 2
+    assert call(lib, x=FAKE + 4) == 6 and call(lib, ids=FAKE + 4) == 6 and call(lib, w=FAKE + 8) == 6
+
+
+@pytest.mark.parametrize("call", [_moe, _layer])
+def test_expert_argument_errors(lib, call):
+    assert call(lib, I=40) == 1 and call(lib, I=0) == 1
+    assert call(lib, T=65) == 2 and call(lib, odt=5) == 2 and call(lib, I=(1 << 19) + 32) == 2
+    for name in ("gq", "gd", "dq", "dd", "y"):
+        assert call(lib, **{name: 0}) == 1 and call(lib, **{name: FAKE + 4}) == 6
+    assert call(lib, ws=0) == 3 and call(lib, wsb=64) == 3 and call(lib, ws=FAKE + 4) == 6
+
+
+def test_router_argument_errors(lib):
+    for call in (_route, _layer):
+        assert call(lib, wr=0) == 1 and call(lib, wr=FAKE + 4) == 6 and call(lib, wdt=9) == 2
+
+
+@pytest.mark.parametrize("shape", [(0, 8, 64, 64, 2), (65, 8, 64, 64, 2), (1, 257, 64, 64, 2), (1, 8, 64, 64, 9),
+                                   (1, 64, 64, 64, 17), (1, 8, 40, 64, 2), (1, 8, 64, 40, 2), (1, 8, 64, 64, 0)])
+def test_workspace_rejects(lib, shape):
+    assert w4a8.w4a8_moe_workspace_bytes(*shape) == 0
+    with pytest.raises(w4a8.W4A8Error):
+        w4a8.moe_workspace(*shape, device="cpu")
+
+
+@pytest.mark.parametrize("T,E,H,I,k", [(1, 1, 32, 32, 1), (64, 64, 2048, 1024, 8), (4, 8, 4096, 14336, 2)])
+def test_workspace_holds_the_activations(lib, T, E, H, I, k):
+    """At least the Q8_0 form (codes and f32 scales) of x and of every slot's h."""
+    assert w4a8.w4a8_moe_workspace_bytes(T, E, H, I, k) >= T * H * 9 // 8 + T * k * I * 9 // 8
+
+
+# ------------------------------------------------------------------ the binding
+def _tensors():
+    T, E, H, I, k = 3, 4, 64, 96, 2
+    u8, i16 = torch.uint8, torch.int16
+    ex = dict(gu_qs=torch.zeros(E, 2 * I, H // 2, dtype=u8), gu_d=torch.zeros(E, 2 * I, H // 32, dtype=i16),
+              dn_qs=torch.zeros(E, H, I // 2, dtype=u8), dn_d=torch.zeros(E, H, I // 32, dtype=i16))
+    r = dict(ids=torch.zeros(T, k, dtype=torch.int32), weights=torch.zeros(T, k))
+    x, wr, ws = torch.zeros(T, H), torch.zeros(E, H), torch.zeros(4096, dtype=u8)
+    y = torch.zeros(T, H, dtype=torch.bfloat16)
+    return [
+        ("w4a8_moe_route", w4a8.w4a8_moe_route, dict(x=x, wr=wr, **r), {"top_k": k}, {"x", "wr"}),
+        ("w4a8_moe_q4_0", w4a8.w4a8_moe_q4_0, dict(x=x, **r, **ex, y=y, ws=ws), {}, {"x", "ids", "gu_qs", "ws"}),
+        ("w4a8_moe_layer_q4_0", w4a8.w4a8_moe_layer_q4_0, dict(x=x, wr=wr, **ex, **r, y=y, ws=ws), {"top_k": k},
+         {"x", "gu_qs", "ws"}),
+    ]
+
+
+@pytest.mark.parametrize("case", _tensors(), ids=lambda c: c[0])
+def test_binding_passes_exact_sizes_and_refuses_short_tensors(fake, case):  # noqa: F811
+    name, fn, tensors, other, free = case
+    fn(**tensors, **other)
+    assert [c[0] for c in fake.calls] == [name]
+    ptrs = {a.value for a in fake.calls[0][1] if isinstance(a, ctypes.c_void_p)}
+    assert {v.data_ptr() for v in tensors.values()} <= ptrs
+    fake.calls.clear()
+    for key, v in tensors.items():
+        if key not in free:
+            with pytest.raises(ValueError, match=rf"libw4a8: {key} holds"):
+                fn(**{**tensors, key: v[:-1].contiguous()}, **other)
+    for key, bad in (("ids", tensors["ids"].long()), ("weights", tensors["weights"].double())):
+        with pytest.raises(ValueError, match=f"libw4a8: {key} is"):
+            fn(**{**tensors, key: bad}, **other)
+    with pytest.raises(ValueError, match="contiguous"):
+        fn(**{**tensors, "x": torch.zeros(64, 3).T}, **other)
+    assert fake.calls == []
