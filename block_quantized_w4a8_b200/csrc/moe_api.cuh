@@ -15,23 +15,21 @@ inline bool moe_supported(int T, int E, int I, int top_k) {
 }
 
 struct MoeWs {
-    int8_t* xq;  // Q8_0 of x
+    uint8_t* xq;  // Q8_0 of x and of every slot's h, in the layout of moe.cuh
     float* xd;
-    float* h;    // experts' activations, one row per slot
-    int8_t* hq;  // Q8_0 of h
+    uint8_t* hq;
     float* hd;
     size_t bytes;
 };
 MoeWs moe_ws(void* ws, int T, int H, int I, int top_k) {
     MoeWs w{};
     char* base = static_cast<char*>(ws);
-    const size_t rows = size_t(T) * top_k;
+    const size_t rows = size_t(T) * top_k, hb = moe::padded_blocks(H), ib = moe::padded_blocks(I);
     size_t off = 0;
-    w.xq = reinterpret_cast<int8_t*>(base + off); off = align256(off + size_t(T) * H);
-    w.xd = reinterpret_cast<float*>(base + off); off = align256(off + size_t(T) * (H / 32) * 4);
-    w.h = reinterpret_cast<float*>(base + off); off = align256(off + rows * I * 4);
-    w.hq = reinterpret_cast<int8_t*>(base + off); off = align256(off + rows * I);
-    w.hd = reinterpret_cast<float*>(base + off); off = align256(off + rows * (I / 32) * 4);
+    w.xq = reinterpret_cast<uint8_t*>(base + off); off = align256(off + T * hb * 32);
+    w.xd = reinterpret_cast<float*>(base + off); off = align256(off + T * hb * 4);
+    w.hq = reinterpret_cast<uint8_t*>(base + off); off = align256(off + rows * ib * 32);
+    w.hd = reinterpret_cast<float*>(base + off); off = align256(off + rows * ib * 4);
     w.bytes = off;
     return w;
 }
@@ -46,20 +44,25 @@ w4a8_status check_route(int T, int E, int H, int top_k, const void* x, w4a8_dtyp
     return W4A8_OK;
 }
 
+// One launch: the router (wr != nullptr) and the Q8_0 form of x (xq != nullptr).
 w4a8_status run_route(int T, int E, int H, int top_k, int renorm, const void* x, w4a8_dtype xdt, const void* wr,
-                      w4a8_dtype wdt, int* ids, float* weights, cudaStream_t stream) {
-    if (xdt == W4A8_BF16) {
-        if (wdt == W4A8_BF16)
-            moe::route_kernel<true, true><<<T, 256, 0, stream>>>(E, H, top_k, renorm, x, wr, ids, weights);
-        else
-            moe::route_kernel<true, false><<<T, 256, 0, stream>>>(E, H, top_k, renorm, x, wr, ids, weights);
-    } else {
-        if (wdt == W4A8_BF16)
-            moe::route_kernel<false, true><<<T, 256, 0, stream>>>(E, H, top_k, renorm, x, wr, ids, weights);
-        else
-            moe::route_kernel<false, false><<<T, 256, 0, stream>>>(E, H, top_k, renorm, x, wr, ids, weights);
-    }
-    return launch_status();
+                      w4a8_dtype wdt, int* ids, float* weights, uint8_t* xq, float* xd, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(T) * moe::kRouteCtas);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = moe::kRouteCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = wr ? 1 : 0;
+    const bool xb = xdt == W4A8_BF16, wb = wdt == W4A8_BF16;
+    auto* kernel = !wr ? (xb ? moe::route_kernel<false, true, false> : moe::route_kernel<false, false, false>)
+                   : xb ? (wb ? moe::route_kernel<true, true, true> : moe::route_kernel<true, true, false>)
+                        : (wb ? moe::route_kernel<true, false, true> : moe::route_kernel<true, false, false>);
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, E, H, top_k, renorm, x, wr, ids, weights, xq, xd));
 }
 
 w4a8_status check_moe(int T, int E, int H, int I, int top_k, const void* x, w4a8_dtype dt, const void* ids,
@@ -76,21 +79,67 @@ w4a8_status check_moe(int T, int E, int H, int I, int top_k, const void* x, w4a8
     return W4A8_OK;
 }
 
-w4a8_status run_experts(int T, int E, int H, int I, int top_k, const void* x, w4a8_dtype dt, const int* ids,
-                        const float* weights, const uint8_t* gq, const uint16_t* gd, const uint8_t* dq,
-                        const uint16_t* dd, w4a8_dtype odt, void* y, void* ws, cudaStream_t stream) {
-    const MoeWs w = moe_ws(ws, T, H, I, top_k);
-    w4a8_status st = run_quant_rowmajor(x, dt, T, H, w.xq, w.xd, nullptr, stream);
-    if (st != W4A8_OK) return st;
-    const int64_t nh = int64_t(T) * top_k * I, ny = int64_t(T) * H;
-    moe::gate_up_simple_kernel<<<unsigned(cdiv(nh, 8)), 256, 0, stream>>>(nh, E, H, I, top_k, w.xq, w.xd, ids, gq, gd,
-                                                                          w.h);
-    if ((st = launch_status()) != W4A8_OK) return st;
-    st = run_quant_rowmajor(w.h, W4A8_F32, T * top_k, I, w.hq, w.hd, nullptr, stream);
-    if (st != W4A8_OK) return st;
-    moe::down_simple_kernel<<<unsigned(cdiv(ny, 8)), 256, 0, stream>>>(ny, E, H, I, top_k, w.hq, w.hd, ids, weights, dq,
-                                                                       dd, y, odt == W4A8_BF16 ? 1 : 0);
-    return launch_status();
+// Tensor maps of Q4_0 rows: codes in boxes of 128 bytes (8 blocks) x 16 rows with the
+// 128-byte swizzle; scales in boxes of 8 x 16, when their rows' pitch allows TMA.
+bool moe_maps(CUtensorMap* tq, CUtensorMap* ts, int* sc_tma, const uint8_t* q, const uint16_t* d, int64_t rows, int K) {
+    *sc_tma = K % 256 == 0 ? 1 : 0;
+    memset(ts, 0, sizeof(*ts));
+    return encode_2d(tq, q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(K / 2), uint64_t(rows), uint64_t(K / 2), 128, 16,
+                     CU_TENSOR_MAP_SWIZZLE_128B) &&
+           (!*sc_tma || encode_2d(ts, d, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, uint64_t(K / 32), uint64_t(rows),
+                                  uint64_t(K / 32) * 2, 8, 16));
+}
+
+template <int NT>
+w4a8_status launch_experts(int T, int E, int H, int I, int top_k, const int* ids, const float* weights,
+                           const uint8_t* gq, const uint16_t* gd, const uint8_t* dq, const uint16_t* dd, int out_bf16,
+                           void* y, const MoeWs& w, cudaStream_t stream) {
+    CUtensorMap gtq, gts, dtq, dts;
+    int gsc, dsc;
+    if (!moe_maps(&gtq, &gts, &gsc, gq, gd, int64_t(E) * 2 * I, H) ||
+        !moe_maps(&dtq, &dts, &dsc, dq, dd, int64_t(E) * H, I))
+        return W4A8_ERR_CUDA;
+    const int n = T * top_k, per_sm = NT <= 2 ? 2 : 1;
+    // limits for the largest lists, so that one setting serves every call
+    constexpr int kMaxSlots = 8 * NT * moe::kMaxTopK;
+    const size_t gs = moe::gate_up_smem(E, n), ds = moe::down_smem(T, E, n);
+    cudaError_t e = smem_limit_once(moe::gate_up_kernel<NT>, int(moe::gate_up_smem(moe::kMaxExperts, kMaxSlots)));
+    if (e == cudaSuccess)
+        e = smem_limit_once(moe::down_kernel<NT>, int(moe::down_smem(8 * NT, moe::kMaxExperts, kMaxSlots)));
+    if (e != cudaSuccess) return cuda_status(e);
+    const int64_t items = int64_t(E < n ? E : n) * (I / 32);
+    const int64_t slots = int64_t(sm_count()) * per_sm;
+    e = launch_pdl(moe::gate_up_kernel<NT>, dim3(unsigned(items < slots ? items : slots)), dim3(256), gs, stream, T, E,
+                   H, I, top_k, ids, (const uint8_t*)w.xq, (const float*)w.xd, gtq, gts, gsc, gd, w.hq, w.hd);
+    if (e != cudaSuccess) return cuda_status(e);
+    int cs = 8;  // the largest cluster whose grid is resident at once
+    while (cs > 1 && int64_t(H / 32) * cs > slots) cs >>= 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(cs), unsigned(H / 32));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = ds;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cs);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, moe::down_kernel<NT>, T, E, H, I, top_k, ids, weights,
+                                          (const uint8_t*)w.hq, (const float*)w.hd, dtq, dts, dsc, dd, y, out_bf16));
+}
+
+w4a8_status run_experts(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* gq,
+                        const uint16_t* gd, const uint8_t* dq, const uint16_t* dd, w4a8_dtype odt, void* y,
+                        const MoeWs& w, cudaStream_t stream) {
+    const int bf = odt == W4A8_BF16 ? 1 : 0;
+    if (T <= 8) return launch_experts<1>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
+    if (T <= 16) return launch_experts<2>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
+    if (T <= 32) return launch_experts<4>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
+    return launch_experts<8>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
 }
 
 }  // namespace
@@ -101,7 +150,7 @@ w4a8_status w4a8_moe_route(int T, int E, int H, int top_k, int renorm, const voi
                            w4a8_dtype wr_dtype, int32_t* ids, float* weights, cudaStream_t stream) {
     const w4a8_status st = check_route(T, E, H, top_k, x, dtype, wr, wr_dtype, ids, weights);
     if (st != W4A8_OK) return st;
-    return run_route(T, E, H, top_k, renorm, x, dtype, wr, wr_dtype, ids, weights, stream);
+    return run_route(T, E, H, top_k, renorm, x, dtype, wr, wr_dtype, ids, weights, nullptr, nullptr, stream);
 }
 
 size_t w4a8_moe_workspace_bytes(int T, int E, int H, int I, int top_k) {
@@ -113,10 +162,13 @@ w4a8_status w4a8_moe_q4_0(int T, int E, int H, int I, int top_k, const void* x, 
                           const float* weights, const uint8_t* gu_qs, const uint16_t* gu_d, const uint8_t* dn_qs,
                           const uint16_t* dn_d, w4a8_dtype out_dtype, void* y, void* ws, size_t ws_bytes,
                           cudaStream_t stream) {
-    const w4a8_status st = check_moe(T, E, H, I, top_k, x, dtype, ids, weights, gu_qs, gu_d, dn_qs, dn_d, out_dtype, y,
-                                     ws, ws_bytes);
+    w4a8_status st = check_moe(T, E, H, I, top_k, x, dtype, ids, weights, gu_qs, gu_d, dn_qs, dn_d, out_dtype, y, ws,
+                               ws_bytes);
     if (st != W4A8_OK) return st;
-    return run_experts(T, E, H, I, top_k, x, dtype, ids, weights, gu_qs, gu_d, dn_qs, dn_d, out_dtype, y, ws, stream);
+    const MoeWs w = moe_ws(ws, T, H, I, top_k);
+    st = run_route(T, E, H, top_k, 0, x, dtype, nullptr, W4A8_F32, nullptr, nullptr, w.xq, w.xd, stream);
+    if (st != W4A8_OK) return st;
+    return run_experts(T, E, H, I, top_k, ids, weights, gu_qs, gu_d, dn_qs, dn_d, out_dtype, y, w, stream);
 }
 
 w4a8_status w4a8_moe_layer_q4_0(int T, int E, int H, int I, int top_k, int renorm, const void* x, w4a8_dtype dtype,
@@ -128,9 +180,10 @@ w4a8_status w4a8_moe_layer_q4_0(int T, int E, int H, int I, int top_k, int renor
     if (st != W4A8_OK) return st;
     st = check_route(T, E, H, top_k, x, dtype, wr, wr_dtype, ids, weights);
     if (st != W4A8_OK) return st;
-    st = run_route(T, E, H, top_k, renorm, x, dtype, wr, wr_dtype, ids, weights, stream);
+    const MoeWs w = moe_ws(ws, T, H, I, top_k);
+    st = run_route(T, E, H, top_k, renorm, x, dtype, wr, wr_dtype, ids, weights, w.xq, w.xd, stream);
     if (st != W4A8_OK) return st;
-    return run_experts(T, E, H, I, top_k, x, dtype, ids, weights, gu_qs, gu_d, dn_qs, dn_d, out_dtype, y, ws, stream);
+    return run_experts(T, E, H, I, top_k, ids, weights, gu_qs, gu_d, dn_qs, dn_d, out_dtype, y, w, stream);
 }
 
 }  // extern "C"
