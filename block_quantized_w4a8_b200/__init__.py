@@ -173,8 +173,9 @@ def _epilogue(bias: torch.Tensor | None, y: torch.Tensor, N: int, dev: int) -> E
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # the current stream's handle, without building a Stream object (3 us)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -407,13 +408,18 @@ def _fp8_scales(N: int, K: int) -> int:
     return -(-N // 128) * -(-K // 128) * 4
 
 
-def _element(t: torch.Tensor, name: str, *dtypes: torch.dtype) -> torch.Tensor:
+_CODES, _F32, _I32 = (torch.float8_e4m3fn, torch.uint8), (torch.float32,), (torch.int32,)
+
+
+def _typed(t: torch.Tensor, dtypes, dev: int, need: int, name: str):
+    """_ptr of a tensor whose element type the call fixes."""
     if t.dtype not in dtypes:
         raise ValueError(f"libw4a8: {name} is {t.dtype}; this call takes {' or '.join(map(str, dtypes))}")
-    return t
+    return _ptr(t, dev, need, name)
 
 
-_CODES = (torch.float8_e4m3fn, torch.uint8)
+# The epilogues without a bias: read by the library during the call only.
+_NO_BIAS = {torch.float32: None, torch.bfloat16: ctypes.byref(Epilogue(None, W4A8_F32, W4A8_BF16))}
 
 
 def w4a8_quant_act_fp8(x, q, s, stream=None) -> None:
@@ -422,8 +428,8 @@ def w4a8_quant_act_fp8(x, q, s, stream=None) -> None:
     dev = _device(x)
     _check("w4a8_quant_act_fp8",
            load_library().w4a8_quant_act_fp8(_ptr(x, dev), _dtype(x), M, K,
-                                             _ptr(_element(q, "q", *_CODES), dev, M * K, "q"),
-                                             _ptr(_element(s, "s", torch.float32), dev, M * -(-K // 128) * 4, "s"),
+                                             _typed(q, _CODES, dev, M * K, "q"),
+                                             _typed(s, _F32, dev, M * -(-K // 128) * 4, "s"),
                                              _stream(stream)))
 
 
@@ -433,8 +439,8 @@ def w4a8_pack_fp8(w, q, s, stream=None) -> None:
     dev = _device(w)
     _check("w4a8_pack_fp8",
            load_library().w4a8_pack_fp8(_ptr(w, dev), _dtype(w), N, K,
-                                        _ptr(_element(q, "q", *_CODES), dev, N * K, "q"),
-                                        _ptr(_element(s, "s", torch.float32), dev, _fp8_scales(N, K), "s"),
+                                        _typed(q, _CODES, dev, N * K, "q"),
+                                        _typed(s, _F32, dev, _fp8_scales(N, K), "s"),
                                         _stream(stream)))
 
 
@@ -447,12 +453,14 @@ def w4a8_gemm_fp8(x, q, s, y, ws, bias=None, stream=None) -> None:
     M, K = x.shape
     N = q.shape[0]
     dev = _device(x)
-    epi = _epilogue(bias, y, N, dev)
+    epi = _NO_BIAS.get(y.dtype) if bias is None else None
+    if bias is not None or y.dtype not in _NO_BIAS:
+        epi = ctypes.byref(_epilogue(bias, y, N, dev))
     _check("w4a8_gemm_fp8",
            load_library().w4a8_gemm_fp8(M, N, K, _ptr(x, dev), _dtype(x),
-                                        _ptr(_element(q, "q", *_CODES), dev, N * K, "q"),
-                                        _ptr(_element(s, "s", torch.float32), dev, _fp8_scales(N, K), "s"),
-                                        ctypes.byref(epi), _ptr(y, dev, M * N * y.element_size(), "y"),
+                                        _typed(q, _CODES, dev, N * K, "q"),
+                                        _typed(s, _F32, dev, _fp8_scales(N, K), "s"),
+                                        epi, _ptr(y, dev, M * N * y.element_size(), "y"),
                                         _ptr(ws, dev), ws.nbytes, _stream(stream)))
 
 
@@ -463,8 +471,8 @@ def w4a8_gemm_fp8_backward(dy, q, s, dx, ws, stream=None) -> None:
     dev = _device(dy)
     _check("w4a8_gemm_fp8_backward",
            load_library().w4a8_gemm_fp8_backward(M, N, K, _ptr(dy, dev), _dtype(dy),
-                                                 _ptr(_element(q, "q", *_CODES), dev, N * K, "q"),
-                                                 _ptr(_element(s, "s", torch.float32), dev, _fp8_scales(N, K), "s"),
+                                                 _typed(q, _CODES, dev, N * K, "q"),
+                                                 _typed(s, _F32, dev, _fp8_scales(N, K), "s"),
                                                  _dtype(dx), _ptr(dx, dev, M * K * dx.element_size(), "dx"),
                                                  _ptr(ws, dev), ws.nbytes, _stream(stream)))
 
@@ -478,8 +486,8 @@ def w4a8_moe_route(x, wr, top_k: int, ids, weights, renorm: bool = True, stream=
     _check("w4a8_moe_route",
            load_library().w4a8_moe_route(T, E, H, top_k, int(renorm), _ptr(x, dev), _dtype(x),
                                          _ptr(wr, dev, E * H * wr.element_size(), "wr"), _dtype(wr),
-                                         _ptr(_element(ids, "ids", torch.int32), dev, n, "ids"),
-                                         _ptr(_element(weights, "weights", torch.float32), dev, n, "weights"),
+                                         _typed(ids, _I32, dev, n, "ids"),
+                                         _typed(weights, _F32, dev, n, "weights"),
                                          _stream(stream)))
 
 
@@ -506,8 +514,8 @@ def w4a8_moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, y, ws, stream=None)
     n = T * top_k * 4
     _check("w4a8_moe_q4_0",
            load_library().w4a8_moe_q4_0(T, E, H, I, top_k, _ptr(x, dev), _dtype(x),
-                                        _ptr(_element(ids, "ids", torch.int32), dev, n, "ids"),
-                                        _ptr(_element(weights, "weights", torch.float32), dev, n, "weights"), *experts,
+                                        _typed(ids, _I32, dev, n, "ids"),
+                                        _typed(weights, _F32, dev, n, "weights"), *experts,
                                         _dtype(y), _ptr(y, dev, T * H * y.element_size(), "y"), _ptr(ws, dev),
                                         ws.nbytes, _stream(stream)))
 
@@ -522,8 +530,8 @@ def w4a8_moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k: int, ids, weight
     _check("w4a8_moe_layer_q4_0",
            load_library().w4a8_moe_layer_q4_0(T, E, H, I, top_k, int(renorm), _ptr(x, dev), _dtype(x),
                                               _ptr(wr, dev, E * H * wr.element_size(), "wr"), _dtype(wr), *experts,
-                                              _ptr(_element(ids, "ids", torch.int32), dev, n, "ids"),
-                                              _ptr(_element(weights, "weights", torch.float32), dev, n, "weights"),
+                                              _typed(ids, _I32, dev, n, "ids"),
+                                              _typed(weights, _F32, dev, n, "weights"),
                                               _dtype(y), _ptr(y, dev, T * H * y.element_size(), "y"), _ptr(ws, dev),
                                               ws.nbytes, _stream(stream)))
 

@@ -25,6 +25,8 @@ namespace moe {
 
 constexpr int kMaxExperts = 256;
 constexpr int kMaxTopK = 16;
+constexpr int kMaxTokens = 64;
+constexpr int kMaxSlotsPerThread = kMaxTokens * kMaxTopK / 256;
 
 // ------------------------------------------------------------------ router
 // Order-preserving map of a float to an unsigned key (larger float, larger key; a NaN of
@@ -35,15 +37,22 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// Eight consecutive elements (idx a multiple of 8), widened to f32.
 template <bool BF16>
 __device__ __forceinline__ void load8f(const void* p, int64_t idx, float (&v)[8]) {
-    float a[4], b[4];
-    load4<BF16>(p, idx, a);
-    load4<BF16>(p, idx + 4, b);
+    if (BF16) {
+        const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p) + idx);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = a[i];
-        v[4 + i] = b[i];
+        for (int i = 0; i < 4; ++i) {  // a bf16 is the top half of an f32
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+        const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + idx);
+        const float4 b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + idx + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     }
 }
 
@@ -75,10 +84,11 @@ __global__ void __launch_bounds__(256) route_kernel(int E, int H, int top_k, int
     const int t = blockIdx.x / kRouteCtas, rank = blockIdx.x % kRouteCtas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
     if (ROUTE) {
-        cluster_sync();  // the first CTA runs: its shared memory can be written
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        bool waited = false;
         for (int e = rank + kRouteCtas * warp; e < E; e += kRouteCtas * 8) {
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
+#pragma unroll 8
             for (int k = lane * 8; k < H; k += 256) {
                 float a[8], b[8];
                 load8f<XB>(x, int64_t(t) * H + k, a);
@@ -89,8 +99,13 @@ __global__ void __launch_bounds__(256) route_kernel(int E, int H, int top_k, int
             float v = (s[0] + s[1]) + (s[2] + s[3]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (!waited) {  // the first CTA runs: its shared memory can be written
+                asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+                waited = true;
+            }
             if (lane == 0) st_cluster(mapa_shared(smem_addr(&logit[e]), 0), v);
         }
+        if (!waited) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     }
     if (xq) {
         const int B = H / 32, Bp = padded_blocks(H), sub = threadIdx.x & 7;
@@ -152,90 +167,124 @@ __global__ void __launch_bounds__(256) route_kernel(int E, int H, int top_k, int
 // ------------------------------------------------------------------ who uses which expert
 // Built by every CTA in shared memory from the T x top_k slots. A slot that names its
 // token's expert again is folded into the first one (their weights added), so a token is at
-// most once in an expert's list.
+// most once in an expert's list. Lists longer than `group` tokens are cut into groups, each a
+// pass of its own over the expert's weights.
 struct Lists {
-    int* off;       // [E + 1] first entry of an expert
-    int* act;       // [E] experts with entries, in rising order
-    int* cur;       // [E] scratch
-    uint16_t* ord;  // [n] slots by expert
-    float* w;       // [n] weight of a slot (folded), by slot
-    int* nact;
+    int* id;         // [n] expert of a slot, -1: empty or folded
+    float* w;        // [n] weight of a slot (folded)
+    int* cur;        // [E] scratch
+    uint16_t* act;   // [max groups] expert of a group, in rising order
+    uint16_t* from;  // first entry of a group
+    uint16_t* ord;   // [n] slots by expert
+    uint8_t* cnt;    // tokens of a group
+    uint8_t* hist;   // [n / 32][E] scratch: tokens of an expert in each 32 slots
+    int* nact;       // groups
 };
-__host__ __device__ __forceinline__ size_t lists_bytes(int E, int n) {
-    return size_t(3 * E + 4) * 4 + size_t(n) * 4 + size_t(n + 7) / 8 * 16;
+__host__ __device__ __forceinline__ int max_groups(int E, int n, int group) { return (E < n ? E : n) + n / group; }
+__host__ __device__ __forceinline__ size_t lists_bytes(int E, int n, int group) {
+    return size_t(E + 1) * 4 + size_t(n) * 8 +
+           (size_t(max_groups(E, n, group)) * 5 + size_t(n) * 2 + size_t(n + 31) / 32 * E + 15) / 16 * 16;
 }
-__device__ __forceinline__ Lists lists_at(uint8_t* p, int E, int n) {
+__device__ __forceinline__ Lists lists_at(uint8_t* p, int E, int n, int group) {
+    const int m = max_groups(E, n, group);
     Lists l;
-    l.off = reinterpret_cast<int*>(p);
-    l.act = l.off + E + 1;
-    l.cur = l.act + E;
+    l.id = reinterpret_cast<int*>(p);
+    l.w = reinterpret_cast<float*>(l.id + n);
+    l.cur = reinterpret_cast<int*>(l.w + n);
     l.nact = l.cur + E;
-    l.w = reinterpret_cast<float*>(l.nact + 3);
-    l.ord = reinterpret_cast<uint16_t*>(l.w + n);
+    l.act = reinterpret_cast<uint16_t*>(l.nact + 1);
+    l.from = l.act + m;
+    l.ord = l.from + m;
+    l.cnt = reinterpret_cast<uint8_t*>(l.ord + n);
+    l.hist = l.cnt + m;
     return l;
 }
-// All threads of the CTA (256) call it; ids (and weights, unless null) are read from L2.
-__device__ __forceinline__ void build_lists(const Lists& l, const int* ids, const float* weights, int n, int top_k, int E) {
-    for (int e = threadIdx.x; e < E; e += 256) l.cur[e] = 0;
-    __syncthreads();
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int i = threadIdx.x; i < n; i += 256) {
-            int id = __ldcg(ids + i);
-            if (id < 0 || id >= E) continue;
-            const int s0 = i / top_k * top_k;
-            bool again = false;
-            for (int s = s0; s < i; ++s) again |= __ldcg(ids + s) == id;
-            if (again) continue;
-            if (pass == 0) {
-                atomicAdd(&l.cur[id], 1);
-                if (weights) {
-                    float w = __ldcg(weights + i);
-                    for (int s = i + 1; s < s0 + top_k; ++s)
-                        if (__ldcg(ids + s) == id) w = __fadd_rn(w, __ldcg(weights + s));
-                    l.w[i] = w;
-                }
-            } else {
-                // the order within an expert's list decides only which MMA column computes a
-                // token, never a sum
-                l.ord[atomicAdd(&l.cur[id], 1)] = uint16_t(i);
-            }
-        }
-        __syncthreads();
-        if (pass == 0 && threadIdx.x < 32) {  // offsets and the list of used experts: 8 experts per lane
-            const int lane = threadIdx.x;
-            int c[8], sum = 0, used = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = lane * 8 + i < E ? l.cur[lane * 8 + i] : 0;
-                sum += c[i];
-                used += c[i] > 0;
-            }
-            int a = sum, u = used;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int pa = __shfl_up_sync(0xffffffffu, a, o), pu = __shfl_up_sync(0xffffffffu, u, o);
-                if (lane >= o) {
-                    a += pa;
-                    u += pu;
-                }
-            }
-            if (lane == 31) {
-                *l.nact = u;
-                l.off[E] = a;
-            }
-            a -= sum;
-            u -= used;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (lane * 8 + i < E) {
-                    l.off[lane * 8 + i] = a;
-                    l.cur[lane * 8 + i] = a;
-                    if (c[i] > 0) l.act[u++] = lane * 8 + i;
-                    a += c[i];
-                }
-        }
-        __syncthreads();
+// Entries stand in the order of the slots, so that every CTA cuts the same groups. All
+// threads of the CTA (256) call it; ids and weights are read from L2.
+__device__ __forceinline__ void build_lists(const Lists& l, const int* ids, const float* weights, int n, int top_k, int E,
+                                            int group) {
+    for (int i = threadIdx.x; i < n; i += 256) {
+        const int id = __ldcg(ids + i);
+        l.id[i] = id >= 0 && id < E ? id : -1;
+        l.w[i] = __ldcg(weights + i);
     }
+    const int chunks = (n + 31) / 32;
+    for (int e = threadIdx.x; e < chunks * E; e += 256) l.hist[e] = 0;
+    __syncthreads();
+    int mine[kMaxSlotsPerThread];
+    int rank[kMaxSlotsPerThread];  // among the 32 slots of this warp's chunk
+    float wsum[kMaxSlotsPerThread];
+#pragma unroll
+    for (int k = 0; k < kMaxSlotsPerThread; ++k) {
+        const int i = threadIdx.x + 256 * k;
+        mine[k] = i < n ? l.id[i] : -1;
+        if (i - int(threadIdx.x & 31) >= n) continue;  // the whole warp
+        if (mine[k] >= 0) {
+            const int s0 = i / top_k * top_k, id = mine[k];
+            wsum[k] = l.w[i];
+            for (int s = s0; s < s0 + top_k; ++s)
+                if (s != i && l.id[s] == id) {
+                    if (s < i) mine[k] = -1;
+                    wsum[k] = __fadd_rn(wsum[k], l.w[s]);
+                }
+        }
+        const uint32_t same = __match_any_sync(0xffffffffu, mine[k]);
+        rank[k] = __popc(same & ((1u << (threadIdx.x & 31)) - 1u));
+        if (mine[k] >= 0 && rank[k] == 0) l.hist[(i >> 5) * E + mine[k]] = uint8_t(__popc(same));
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += 256) {
+        int run = 0;
+        for (int c = 0; c < chunks; ++c) {
+            const int h = l.hist[c * E + e];
+            l.hist[c * E + e] = uint8_t(run);
+            run += h;
+        }
+        l.cur[e] = run;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {  // first entries and groups: 8 experts per lane
+        const int lane = threadIdx.x;
+        int c[8], sum = 0, used = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            c[i] = lane * 8 + i < E ? l.cur[lane * 8 + i] : 0;
+            sum += c[i];
+            used += (c[i] + group - 1) / group;
+        }
+        int a = sum, u = used;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int pa = __shfl_up_sync(0xffffffffu, a, o), pu = __shfl_up_sync(0xffffffffu, u, o);
+            if (lane >= o) {
+                a += pa;
+                u += pu;
+            }
+        }
+        if (lane == 31) *l.nact = u;
+        a -= sum;
+        u -= used;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (lane * 8 + i < E) {
+                l.cur[lane * 8 + i] = a;
+                for (int g = 0; g < c[i]; g += group, ++u) {
+                    l.act[u] = uint16_t(lane * 8 + i);
+                    l.from[u] = uint16_t(a + g);
+                    l.cnt[u] = uint8_t(min(group, c[i] - g));
+                }
+                a += c[i];
+            }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMaxSlotsPerThread; ++k)
+        if (mine[k] >= 0) {
+            const int i = threadIdx.x + 256 * k;
+            l.ord[l.cur[mine[k]] + l.hist[(i >> 5) * E + mine[k]] + rank[k]] = uint16_t(i);
+            l.w[i] = wsum[k];
+        }
+    __syncthreads();
 }
 
 // ------------------------------------------------------------------ the weight stream
@@ -415,17 +464,17 @@ __device__ __forceinline__ void init_ctrl(Ctrl* ctrl) {
 // ------------------------------------------------------------------ gate, up and h
 constexpr int kRedPitch = 9;
 constexpr int kRedBytes = 4 * 64 * kRedPitch * 4;
-__host__ __device__ __forceinline__ size_t gate_up_smem(int E, int n) {
-    return 1024 + kRingBytes + kCtrlBytes + kRedBytes + lists_bytes(E, n);
+__host__ __device__ __forceinline__ size_t gate_up_smem(int E, int n, int group) {
+    return 1024 + kRingBytes + kCtrlBytes + kRedBytes + lists_bytes(E, n, group);
 }
 
-// Items: (used expert, 32 rows of I), dealt round-robin to the CTAs. Two warps share a
+// Items: (32 rows of I, group of tokens of one expert), dealt round-robin to the CTAs. Two warps share a
 // K slice's boxes (one per 16 gate and 16 up rows), four slices; their sums meet in shared
-// memory, where a warp per token forms h, its block's scale and codes. NT: most 8-token tiles
-// of one expert handled in one pass over the weights.
+// memory, where a warp per token forms h, its block's scale and codes. NT:
+// 8-token tiles of a group.
 template <int NT>
-__global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
-    gate_up_kernel(int T, int E, int H, int I, int top_k, const int* ids, const uint8_t* xq, const float* xd,
+__global__ void __launch_bounds__(256, 2)
+    gate_up_kernel(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* xq, const float* xd,
                    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_s, int sc_tma,
                    const uint16_t* __restrict__ wd, uint8_t* __restrict__ hq, float* __restrict__ hd) {
     extern __shared__ uint8_t smem_raw[];
@@ -433,19 +482,19 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + kRingBytes);
     float* red = reinterpret_cast<float*>(smem + kRingBytes + kCtrlBytes);
     const int n = T * top_k;
-    const Lists l = lists_at(smem + kRingBytes + kCtrlBytes + kRedBytes, E, n);
+    const Lists l = lists_at(smem + kRingBytes + kCtrlBytes + kRedBytes, E, n, 8 * NT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rg = warp & 1, ksl = warp >> 1;
     init_ctrl(ctrl);
     pdl_wait_primary();  // ids, xq and xd are written by the preceding kernel
     pdl_launch_dependents();
-    build_lists(l, ids, nullptr, n, top_k, E);  // its barriers also publish the control block
+    build_lists(l, ids, weights, n, top_k, E, 8 * NT);  // its barriers also publish the control block
     const int B = H / 32, Bp = padded_blocks(H), nbox = Bp / kBoxBlocks;
     const int IB = I / 32, IBp = padded_blocks(I);
     const int nitems = *l.nact * IB;
     Ring ring = make_ring(smem, ctrl);
     int pi = blockIdx.x, pj = ksl;  // the next box to fetch: item, box
-    auto row_of = [&](int item) { return l.act[item / IB] * 2 * I + (item % IB) * 32 + rg * 16; };
+    auto row_of = [&](int item) { return int(l.act[item / IB]) * 2 * I + (item % IB) * 32 + rg * 16; };
     auto fetch = [&]() {
         if (ksl >= nbox || pi >= nitems || ring.dead) return;
         if (lane == 0) {
@@ -463,10 +512,9 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
     for (int s = 0; s < kStages; ++s) fetch();
 
     for (int item = blockIdx.x; item < nitems; item += gridDim.x) {
-        const int e = l.act[item / IB], ib = item % IB;
-        const int first = l.off[e], cnt = l.off[e + 1] - first;
+        const int gi = item / IB, ib = item - gi * IB;
+        const int first = l.from[gi], cnt = l.cnt[gi], nt = (cnt + 7) / 8;
         const int r = row_of(item);
-        const int nt = (cnt + 7) / 8;  // at most NT: a list holds a token once, and the host has T <= 8 NT
         Rows<NT> rows;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -531,8 +579,8 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
 
 // ------------------------------------------------------------------ down and the weighted sum
 constexpr int kYPitch = 33;
-__host__ __device__ __forceinline__ size_t down_smem(int T, int E, int n) {
-    return 1024 + kRingBytes + kCtrlBytes + size_t(kWarps) * T * kYPitch * 4 + lists_bytes(E, n);
+__host__ __device__ __forceinline__ size_t down_smem(int T, int E, int n, int group) {
+    return 1024 + kRingBytes + kCtrlBytes + size_t(kWarps) * T * kYPitch * 4 + lists_bytes(E, n, group);
 }
 
 // Grid: x = split (the cluster), y = 32 rows of H. The boxes of all used experts for those
@@ -540,7 +588,7 @@ __host__ __device__ __forceinline__ size_t down_smem(int T, int E, int n) {
 // slots' weights, to a [token][row] array of its own, and the arrays are added in a fixed
 // order (within the CTA, then across the cluster through distributed shared memory).
 template <int NT>
-__global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(256, 2)
     down_kernel(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* hq,
                 const float* hd, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_s,
                 int sc_tma, const uint16_t* __restrict__ wd, void* __restrict__ y, int out_bf16) {
@@ -549,7 +597,7 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + kRingBytes);
     float* ybuf = reinterpret_cast<float*>(smem + kRingBytes + kCtrlBytes);
     const int n = T * top_k, YT = T * kYPitch;
-    const Lists l = lists_at(reinterpret_cast<uint8_t*>(ybuf + kWarps * YT), E, n);
+    const Lists l = lists_at(reinterpret_cast<uint8_t*>(ybuf + kWarps * YT), E, n, 8 * NT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n0 = blockIdx.y * 32, slices = gridDim.x * kWarps;
     init_ctrl(ctrl);
@@ -557,7 +605,7 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
     // Read before the wait: ids and weights come from the kernel before the preceding one,
     // which has completed, since every CTA of the preceding kernel waits for it before it
     // lets this grid start (and the loads are from L2).
-    build_lists(l, ids, weights, n, top_k, E);
+    build_lists(l, ids, weights, n, top_k, E, 8 * NT);
     const int B = I / 32, Bp = padded_blocks(I), nbox = Bp / kBoxBlocks;
     const int nchunks = *l.nact * nbox;
     Ring ring = make_ring(smem, ctrl);
@@ -565,7 +613,7 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
     auto fetch = [&]() {
         if (pc >= nchunks || ring.dead) return;
         if (lane == 0) {
-            const int r = l.act[pc / nbox] * H + n0;
+            const int r = int(l.act[pc / nbox]) * H + n0;
             ring.issue(&tm_q, &tm_s, sc_tma, pc % nbox, r, r + 16);
         }
         ++ring.issued;
@@ -604,8 +652,8 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
         if (an != a) {
             if (a >= 0) flush();
             a = an;
-            first = l.off[l.act[a]];
-            cnt = l.off[l.act[a] + 1] - first;
+            first = l.from[a];
+            cnt = l.cnt[a];
             nt = (cnt + 7) / 8;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
@@ -616,7 +664,7 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1)
             }
             acc.clear();
         }
-        const int r = l.act[a] * H + n0;
+        const int r = int(l.act[a]) * H + n0;
         ring.wait(wd, sc_tma, j, r, r + 16, B, &ctrl->abort);
         const int st = ring.used % kStages;
         box_dots<NT>(acc, ring.codes + st * kStageBytes, ring.scales + st * kScaleBytes, hq + j * 256,

@@ -99,18 +99,19 @@ w4a8_status launch_experts(int T, int E, int H, int I, int top_k, const int* ids
     if (!moe_maps(&gtq, &gts, &gsc, gq, gd, int64_t(E) * 2 * I, H) ||
         !moe_maps(&dtq, &dts, &dsc, dq, dd, int64_t(E) * H, I))
         return W4A8_ERR_CUDA;
-    const int n = T * top_k, per_sm = NT <= 2 ? 2 : 1;
+    const int n = T * top_k, group = 8 * NT;
+    const size_t gs = moe::gate_up_smem(E, n, group), ds = moe::down_smem(T, E, n, group);
     // limits for the largest lists, so that one setting serves every call
-    constexpr int kMaxSlots = 8 * NT * moe::kMaxTopK;
-    const size_t gs = moe::gate_up_smem(E, n), ds = moe::down_smem(T, E, n);
-    cudaError_t e = smem_limit_once(moe::gate_up_kernel<NT>, int(moe::gate_up_smem(moe::kMaxExperts, kMaxSlots)));
+    constexpr int kT = NT == 1 ? 8 : moe::kMaxTokens;
+    cudaError_t e = smem_limit_once(moe::gate_up_kernel<NT>,
+                                    int(moe::gate_up_smem(moe::kMaxExperts, kT * moe::kMaxTopK, group)));
     if (e == cudaSuccess)
-        e = smem_limit_once(moe::down_kernel<NT>, int(moe::down_smem(8 * NT, moe::kMaxExperts, kMaxSlots)));
+        e = smem_limit_once(moe::down_kernel<NT>, int(moe::down_smem(kT, moe::kMaxExperts, kT * moe::kMaxTopK, group)));
     if (e != cudaSuccess) return cuda_status(e);
-    const int64_t items = int64_t(E < n ? E : n) * (I / 32);
-    const int64_t slots = int64_t(sm_count()) * per_sm;
+    const int64_t items = int64_t(moe::max_groups(E, n, group)) * (I / 32);
+    const int64_t slots = int64_t(sm_count()) * 2;
     e = launch_pdl(moe::gate_up_kernel<NT>, dim3(unsigned(items < slots ? items : slots)), dim3(256), gs, stream, T, E,
-                   H, I, top_k, ids, (const uint8_t*)w.xq, (const float*)w.xd, gtq, gts, gsc, gd, w.hq, w.hd);
+                   H, I, top_k, ids, weights, (const uint8_t*)w.xq, (const float*)w.xd, gtq, gts, gsc, gd, w.hq, w.hd);
     if (e != cudaSuccess) return cuda_status(e);
     int cs = 8;  // the largest cluster whose grid is resident at once
     while (cs > 1 && int64_t(H / 32) * cs > slots) cs >>= 1;
@@ -137,9 +138,7 @@ w4a8_status run_experts(int T, int E, int H, int I, int top_k, const int* ids, c
                         const MoeWs& w, cudaStream_t stream) {
     const int bf = odt == W4A8_BF16 ? 1 : 0;
     if (T <= 8) return launch_experts<1>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
-    if (T <= 16) return launch_experts<2>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
-    if (T <= 32) return launch_experts<4>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
-    return launch_experts<8>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
+    return launch_experts<2>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
 }
 
 }  // namespace

@@ -63,7 +63,7 @@ def verify(x, gu, dn, ids, weights, out, rel, what=""):
 # tiles, more tokens per expert than one tile of 8, all 64 tokens on one expert
 SHAPES = [(1, 1, 32, 32, 1), (1, 8, 512, 96, 2), (2, 3, 96, 32, 2), (3, 5, 160, 224, 3), (5, 4, 256, 256, 1),
           (13, 11, 736, 352, 3), (16, 2, 512, 512, 2), (40, 3, 288, 128, 2), (64, 1, 256, 64, 1), (64, 16, 512, 256, 8),
-          (1, 64, 2048, 1024, 8), (9, 2, 4096, 288, 1)]
+          (1, 64, 2048, 1024, 8), (9, 2, 4096, 288, 1), (64, 9, 512, 1024, 5), (33, 4, 96, 2048, 4), (64, 256, 128, 64, 16)]
 
 
 @pytest.mark.parametrize("T,E,H,I,k", SHAPES)
