@@ -4,16 +4,19 @@
 //   output   y[t] = sum over slots s of p[t][s] * (hq[t][s] . Wd[e(t, s)]^T)
 // with the block dots of w4a8_gemm (exact integers, rescaled per 32-block in f32).
 //
-// Three launches: route (one cluster per token; also quantises x), gate_up (g, u, h and its
-// Q8_0 form) and down (the weighted sum). The weights of the chosen experts are read once and
-// are nearly all the traffic, so both expert kernels are built around the stream: every warp
-// runs a ring of TMA boxes of its own (32 rows x 8 blocks), with no barrier between warps
-// until its rows are summed. The dots are mma.sync.m16n8k32 on int8, one per 16 rows and
-// quant block: the instruction's K is the block, its A fragment is the packed codes as they
-// lie in memory (one ldmatrix word holds the low and high nibbles of both K halves), and 8
-// tokens cost what one costs. tcgen05 would need the codes expanded to shared or tensor
-// memory first, and reads its accumulators back per block; at these sizes the memory is the
-// bound, not the matrix rate.
+// Three launches, chained by programmatic dependent launch: route (the router, a cluster per
+// token, and the Q8_0 form of x), gate_up (g, u, h and its Q8_0 form) and down (the weighted
+// sum).
+//
+// The weights of the chosen experts are read once and are nearly all the traffic, so both
+// expert kernels are built around their stream: every warp runs a ring of its own, two TMA boxes
+// (16 rows x 8 blocks each) per stage, with no barrier between warps until their rows are
+// summed. The integer dots are exact. Groups of one or two tokens use dp4a, a row per lane;
+// larger ones mma.sync.m16n8k32 on int8, one per 16 rows and quant block: the instruction's K
+// is the block, its A fragment is the packed codes as they lie in memory (one ldmatrix word
+// holds the low and high nibbles of both K halves), and 8 tokens cost what one costs. tcgen05
+// would need the codes expanded to shared or tensor memory first, and reads its accumulators
+// back per block; at these sizes the memory is the bound, not the matrix rate.
 #pragma once
 
 #include <cuda.h>
@@ -76,11 +79,13 @@ constexpr int kRouteCtas = 8;  // CTAs per token (the cluster)
 // blocks (xq != nullptr) and, with ROUTE, computes the logits of its experts, a warp each;
 // they meet in the first CTA's shared memory, where one warp takes the top_k.
 template <bool ROUTE, bool XB, bool WB>
-__global__ void __launch_bounds__(256) route_kernel(int E, int H, int top_k, int renorm, const void* __restrict__ x,
+__global__ void __launch_bounds__(256, 1) route_kernel(int E, int H, int top_k, int renorm, const void* __restrict__ x,
                                                     const void* __restrict__ wr, int* __restrict__ ids,
                                                     float* __restrict__ weights, uint8_t* __restrict__ xq,
                                                     float* __restrict__ xd) {
     __shared__ float logit[kMaxExperts];
+    __shared__ __align__(16) uint32_t keys[kMaxExperts];
+    __shared__ int chosen[kMaxTopK];
     const int t = blockIdx.x / kRouteCtas, rank = blockIdx.x % kRouteCtas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
     if (ROUTE) {
@@ -106,6 +111,9 @@ __global__ void __launch_bounds__(256) route_kernel(int E, int H, int top_k, int
             if (lane == 0) st_cluster(mapa_shared(smem_addr(&logit[e]), 0), v);
         }
         if (!waited) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        // the logits are on their way; this CTA's codes are written while they arrive (the
+        // release orders stores before it: the codes' global stores come after)
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
     if (xq) {
         const int B = H / 32, Bp = padded_blocks(H), sub = threadIdx.x & 7;
@@ -127,41 +135,40 @@ __global__ void __launch_bounds__(256) route_kernel(int E, int H, int top_k, int
         }
     }
     if (!ROUTE) return;
-    cluster_sync();  // the logits are in the first CTA
-    if (rank != 0 || warp != 0) return;
-    uint32_t key[kMaxExperts / 32];
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) key[i] = lane + 32 * i < E ? order_key(logit[lane + 32 * i]) : 0u;
-    uint32_t taken = 0u;  // bit i: this lane's expert lane + 32 i is chosen
-    float top = 0.0f, sum = 0.0f, mine = 0.0f;
-    for (int s = 0; s < top_k; ++s) {
-        uint32_t best = 0u;
-        unsigned at = 0x7fffffffu;
-#pragma unroll
-        for (int i = kMaxExperts / 32 - 1; i >= 0; --i)  // the lowest index among equals
-            if (lane + 32 * i < E && !((taken >> i) & 1u) && key[i] >= best) {
-                best = key[i];
-                at = unsigned(lane + 32 * i);
-            }
-        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-        const int e = int(__reduce_min_sync(0xffffffffu, best == m ? at : 0x7fffffffu));
-        if ((e & 31) == lane) taken |= 1u << (e >> 5);
-        const float l = logit[e];
-        if (s == 0) top = l;
-        const float p = expf(l - top);
-        sum += p;
-        if (lane == s) {
-            mine = p;
-            ids[int64_t(t) * top_k + s] = e;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank != 0) return;
+    // An expert's rank is the number of experts before it (larger, or equal with a lower
+    // index): no chain of dependent maxima.
+    for (int e = threadIdx.x; e < (E + 3) / 4 * 4; e += 256) keys[e] = e < E ? order_key(logit[e]) : 0u;
+    __syncthreads();
+    if (threadIdx.x < E) {
+        const int me = threadIdx.x;
+        const uint32_t key = keys[me];
+        int before = 0;
+#pragma unroll 4
+        for (int e = 0; e < E; e += 4) {  // keys are below 2^32 - 1; the padding stands behind every expert
+            const uint4 k = *reinterpret_cast<const uint4*>(keys + e);
+            before += int(k.x >= key + (e >= me ? 1u : 0u)) + int(k.y >= key + (e + 1 >= me ? 1u : 0u)) +
+                      int(k.z >= key + (e + 2 >= me ? 1u : 0u)) + int(k.w >= key + (e + 3 >= me ? 1u : 0u));
         }
+        if (before < top_k) chosen[before] = me;
     }
+    __syncthreads();
+    if (warp != 0) return;
+    const int mine = lane < top_k ? chosen[lane] : 0;
+    const float top = logit[chosen[0]];
+    const float p = lane < top_k ? expf(logit[mine] - top) : 0.0f;
+    float sum = p;
     if (!renorm) {
         sum = 0.0f;
         for (int e = lane; e < E; e += 32) sum += expf(logit[e] - top);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    if (lane < top_k) weights[int64_t(t) * top_k + lane] = __fdiv_rn(mine, sum);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane < top_k) {
+        ids[int64_t(t) * top_k + lane] = mine;
+        weights[int64_t(t) * top_k + lane] = __fdiv_rn(p, sum);
+    }
 }
 
 // ------------------------------------------------------------------ who uses which expert
@@ -170,39 +177,86 @@ __global__ void __launch_bounds__(256) route_kernel(int E, int H, int top_k, int
 // most once in an expert's list. Lists longer than `group` tokens are cut into groups, each a
 // pass of its own over the expert's weights.
 struct Lists {
-    int* id;         // [n] expert of a slot, -1: empty or folded
     float* w;        // [n] weight of a slot (folded)
-    int* cur;        // [E] scratch
-    uint16_t* act;   // [max groups] expert of a group, in rising order
-    uint16_t* from;  // first entry of a group
     uint16_t* ord;   // [n] slots by expert
-    uint8_t* cnt;    // tokens of a group
-    uint8_t* hist;   // [n / 32][E] scratch: tokens of an expert in each 32 slots
+    uint16_t* act;   // [groups] expert of a group, in rising order
+    uint16_t* from;  // [groups] first entry
+    uint8_t* cnt;    // [groups] tokens
     int* nact;       // groups
+    int* id;         // scratch: [n] expert of a slot, -1: empty or folded
+    int* cur;        // scratch: [E]
+    uint8_t* hist;   // scratch: [n / 32][E] tokens of an expert in each 32 slots
 };
 __host__ __device__ __forceinline__ int max_groups(int E, int n, int group) { return (E < n ? E : n) + n / group; }
 __host__ __device__ __forceinline__ size_t lists_bytes(int E, int n, int group) {
-    return size_t(E + 1) * 4 + size_t(n) * 8 +
-           (size_t(max_groups(E, n, group)) * 5 + size_t(n) * 2 + size_t(n + 31) / 32 * E + 15) / 16 * 16;
+    return 16 + size_t(n) * 4 + (size_t(max_groups(E, n, group)) * 5 + size_t(n) * 2 + 15) / 16 * 16;
 }
-__device__ __forceinline__ Lists lists_at(uint8_t* p, int E, int n, int group) {
+// `scratch`: at most 4 n + 4 E + E n / 32 bytes (13 KB), free once the lists are built.
+__device__ __forceinline__ Lists lists_at(uint8_t* p, uint8_t* scratch, int E, int n, int group) {
     const int m = max_groups(E, n, group);
     Lists l;
-    l.id = reinterpret_cast<int*>(p);
-    l.w = reinterpret_cast<float*>(l.id + n);
-    l.cur = reinterpret_cast<int*>(l.w + n);
-    l.nact = l.cur + E;
-    l.act = reinterpret_cast<uint16_t*>(l.nact + 1);
+    l.nact = reinterpret_cast<int*>(p);
+    l.w = reinterpret_cast<float*>(p + 16);
+    l.ord = reinterpret_cast<uint16_t*>(l.w + n);
+    l.act = l.ord + n;
     l.from = l.act + m;
-    l.ord = l.from + m;
-    l.cnt = reinterpret_cast<uint8_t*>(l.ord + n);
-    l.hist = l.cnt + m;
+    l.cnt = reinterpret_cast<uint8_t*>(l.from + m);
+    l.id = reinterpret_cast<int*>(scratch);
+    l.cur = l.id + n;
+    l.hist = reinterpret_cast<uint8_t*>(l.cur + E);
     return l;
 }
 // Entries stand in the order of the slots, so that every CTA cuts the same groups. All
-// threads of the CTA (256) call it; ids and weights are read from L2.
+// threads of the CTA call it and pass a barrier after it; ids and weights are read from
+// L2.
 __device__ __forceinline__ void build_lists(const Lists& l, const int* ids, const float* weights, int n, int top_k, int E,
                                             int group) {
+    if (n <= 32 && n <= group * top_k) {  // one warp, one slot per lane, one group per expert
+        if (threadIdx.x < 32) {
+            const int lane = threadIdx.x, id = lane < n ? __ldcg(ids + lane) : -1;
+            float w = lane < n ? __ldcg(weights + lane) : 0.0f;
+            const int t = lane / top_k;
+            bool valid = id >= 0 && id < E;
+            int pos = 0, grp = 0, cnt = 0, groups = 0;  // entries before this one, groups before it, its group's size
+            uint32_t lead = 0u;                          // slots that open a group
+            bool folded = false;
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) {  // fold repeats within a token into the first
+                const int idj = __shfl_sync(0xffffffffu, id, j);
+                const float wj = __shfl_sync(0xffffffffu, w, j);
+                const int tj = __shfl_sync(0xffffffffu, t, j);
+                if (j != lane && tj == t && idj == id) {
+                    if (j < lane)
+                        folded = true;
+                    else
+                        w = __fadd_rn(w, wj);
+                }
+            }
+            valid = valid && !folded;
+            const int key = valid ? id : 0x7fffffff;
+            const uint32_t same = __match_any_sync(0xffffffffu, key);
+            lead = __ballot_sync(0xffffffffu, valid && (same & ((1u << lane) - 1u)) == 0u);
+            cnt = __popc(same);
+            groups = __popc(lead);
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) {
+                const int kj = __shfl_sync(0xffffffffu, key, j);
+                pos += kj < key || (kj == key && j < lane);
+                grp += kj < key && ((lead >> j) & 1u);
+            }
+            if (valid) {
+                l.ord[pos] = uint16_t(lane);
+                l.w[lane] = w;
+                if ((lead >> lane) & 1u) {
+                    l.act[grp] = uint16_t(id);
+                    l.from[grp] = uint16_t(pos);
+                    l.cnt[grp] = uint8_t(cnt);
+                }
+            }
+            if (lane == 0) *l.nact = groups;
+        }
+        return;
+    }
     for (int i = threadIdx.x; i < n; i += 256) {
         const int id = __ldcg(ids + i);
         l.id[i] = id >= 0 && id < E ? id : -1;
@@ -284,17 +338,18 @@ __device__ __forceinline__ void build_lists(const Lists& l, const int* ids, cons
             l.ord[l.cur[mine[k]] + l.hist[(i >> 5) * E + mine[k]] + rank[k]] = uint16_t(i);
             l.w[i] = wsum[k];
         }
-    __syncthreads();
 }
 
-// ------------------------------------------------------------------ the weight stream
+// ------------------------------------------------------------------ the stream
 constexpr int kWarps = 8;
-constexpr int kStages = 2;         // boxes in flight per warp
+constexpr int kGroup = 8;          // tokens of a group: the MMA's columns
+constexpr int kStages = 2;
 constexpr int kBoxBlocks = 8;      // quant blocks per box
 constexpr int kTileBytes = 2048;   // 16 rows x 8 blocks of codes, 128-byte swizzle
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kScaleBytes = 512;   // 2 x 16 rows x 8 fp16
 constexpr int kRingBytes = kWarps * kStages * (kStageBytes + kScaleBytes);
+constexpr int kDp4aTokens = 2;     // largest group on dp4a (see row_dp4a)
 
 // One warp's ring: two 16-row tiles of 8 blocks per stage.
 struct Ring {
@@ -320,18 +375,16 @@ struct Ring {
     // bytes) the warp fetches the box's scales itself, zeros past the row.
     __device__ __forceinline__ void wait(const uint16_t* wd, int sc_tma, int j, int r0, int r1, int B, volatile uint32_t* abort) {
         const int st = used % kStages, lane = threadIdx.x & 31;
-        uint32_t h[4] = {0u, 0u, 0u, 0u};
         if (!sc_tma) {
+            uint32_t h[4] = {0u, 0u, 0u, 0u};
             const uint16_t* src = wd + int64_t((lane < 16 ? r0 : r1) + (lane & 15)) * B + j * kBoxBlocks;
 #pragma unroll
             for (int i = 0; i < kBoxBlocks; ++i)
                 if (j * kBoxBlocks + i < B) h[i >> 1] |= uint32_t(__ldg(src + i)) << (16 * (i & 1));
-        }
-        if (!dead && !bounded_wait_warp(bars + st * 8, (used / kStages) & 1, abort)) dead = true;
-        if (!sc_tma) {
             *reinterpret_cast<uint4*>(scales + st * kScaleBytes + lane * 16) = make_uint4(h[0], h[1], h[2], h[3]);
             __syncwarp();
         }
+        if (!dead && !bounded_wait_warp(bars + st * 8, (used / kStages) & 1, abort)) dead = true;
     }
     __device__ __forceinline__ void drain() {
         for (int i = used; i < issued; ++i) drain_wait_warp(bars + (i % kStages) * 8, (i / kStages) & 1, 200000ull);
@@ -360,76 +413,131 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-__device__ __forceinline__ float half_at(const uint4& v, int i) {
-    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
-    return __half2float(__ushort_as_half(uint16_t((i & 1) ? w >> 16 : w & 0xFFFFu)));
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// Signed bytes 16 (q - 8) of the low (elements 0..15 of the block) and high nibbles.
+__device__ __forceinline__ uint32_t low_codes(uint32_t r) { return ((r << 4) & 0xF0F0F0F0u) ^ 0x80808080u; }
+__device__ __forceinline__ uint32_t high_codes(uint32_t r) { return (r & 0xF0F0F0F0u) ^ 0x80808080u; }
+__device__ __forceinline__ float2 halves(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+
+// Activations of a group: codes and scales of the token in column i at xq + row[i] * pitch and
+// xd + row[i] * pitch / 32. L2: read past L1 (not used twice by an SM).
+template <bool L2>
+__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
+    return L2 ? __ldcg(reinterpret_cast<const uint4*>(p)) : *reinterpret_cast<const uint4*>(p);
+}
+template <bool L2>
+__device__ __forceinline__ float4 load_scales(const float* p) {
+    return L2 ? __ldcg(reinterpret_cast<const float4*>(p)) : *reinterpret_cast<const float4*>(p);
 }
 
-// Accumulators of a warp: per 8-token tile, for each of the two 16-row tiles, the pairs of
-// tokens 2c, 2c+1 (c = lane & 3) of rows lane/4 and lane/4 + 8.
-template <int NT>
-struct Acc {
-    unsigned long long v[NT][2][2];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) v[i][m >> 1][m & 1] = 0ull;
-    }
+// This lane's part of a box of 8 tokens: B fragments (column lane/4) and scales (columns 2c,
+// 2c+1) of its 8 blocks.
+struct Frag {
+    uint4 x[4];
+    float4 d[4];  // [half box][column]
 };
-// Rows of the activation matrix this lane reads for each 8-token tile: column lane/4 of the B
-// fragment, columns 2c and 2c+1 for the scales. Columns past the list repeat its last entry.
-template <int NT>
-struct Rows {
-    int b[NT], s0[NT], s1[NT];
-};
-
-// One box: 32 rows x 8 blocks times nt tiles of 8 tokens; xq, xd already at the box's columns.
-// Per block the integer dot D is exact and enters as round(D * d_w) * d_x, added in f32.
-template <int NT>
-__device__ __forceinline__ void box_dots(Acc<NT>& acc, uint32_t codes, const uint8_t* scales, const uint8_t* xq,
-                                         const float* xd, int pitch, int spitch, const Rows<NT>& rows, int nt) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint32_t base = codes + uint32_t(lane >> 4) * kTileBytes + uint32_t((lane & 15) * 128);
-    uint4 sw[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) sw[m] = *reinterpret_cast<const uint4*>(scales + (m >> 1) * 256 + (g + (m & 1) * 8) * 16);
+template <bool L2>
+__device__ __forceinline__ Frag load_frag(const uint8_t* xb, const float* d0, const float* d1) {
+    Frag f;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        uint32_t a[4][8];
+        f.x[2 * q] = load_codes<L2>(xb + q * 128);
+        f.x[2 * q + 1] = load_codes<L2>(xb + q * 128 + 16);
+        f.d[2 * q] = load_scales<L2>(d0 + q * 4);
+        f.d[2 * q + 1] = load_scales<L2>(d1 + q * 4);
+    }
+    return f;
+}
+
+// One stage: 2 x 16 rows x 8 blocks times 8 tokens. acc[m][h] pairs tokens 2c, 2c+1 (c = lane &
+// 3) of row lane/4 + 8 h of tile m. Per block D is exact, and acc += D * (d_w * d_x).
+__device__ __forceinline__ void stage_mma(unsigned long long (&acc)[2][2], uint32_t codes, const uint8_t* scales,
+                                          const Frag& f) {
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    const uint32_t base = codes + uint32_t(lane >> 4) * kTileBytes + uint32_t((lane & 15) * 128);
+    const unsigned long long magic = pack2(-kMagic, -kMagic);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint2 sw[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            sw[m] = *reinterpret_cast<const uint2*>(scales + (m >> 1) * 256 + (g + (m & 1) * 8) * 16 + q * 8);
+        const uint32_t bw[8] = {f.x[2 * q].x,     f.x[2 * q].y,     f.x[2 * q].z,     f.x[2 * q].w,
+                                f.x[2 * q + 1].x, f.x[2 * q + 1].y, f.x[2 * q + 1].z, f.x[2 * q + 1].w};
+        const float e0[4] = {f.d[2 * q].x, f.d[2 * q].y, f.d[2 * q].z, f.d[2 * q].w};
+        const float e1[4] = {f.d[2 * q + 1].x, f.d[2 * q + 1].y, f.d[2 * q + 1].z, f.d[2 * q + 1].w};
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             uint32_t r[4];
             ldmatrix4(base + uint32_t(((q * 4 + b) ^ (lane & 7)) << 4), r);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {  // 16 (q - 8) as signed bytes: low nibbles (K 0..15), high nibbles (K 16..31)
-                a[b][(m >> 1) * 4 + (m & 1)] = ((r[m] << 4) & 0xF0F0F0F0u) ^ 0x80808080u;
-                a[b][(m >> 1) * 4 + 2 + (m & 1)] = (r[m] & 0xF0F0F0F0u) ^ 0x80808080u;
+            for (int m = 0; m < 2; ++m) {
+                float v[4];
+                mma_s8(v, low_codes(r[2 * m]), low_codes(r[2 * m + 1]), high_codes(r[2 * m]), high_codes(r[2 * m + 1]),
+                       bw[2 * b], bw[2 * b + 1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 p = halves(b < 2 ? sw[2 * m + h].x : sw[2 * m + h].y);
+                    const float w = (b & 1) ? p.y : p.x;
+                    acc[m][h] = fma2(add2(pack2(v[2 * h], v[2 * h + 1]), magic),
+                                     pack2(__fmul_rn(w, e0[b]), __fmul_rn(w, e1[b])), acc[m][h]);
+                }
             }
         }
+    }
+}
+
+// The same stage for CNT tokens (1 or 2), a row per lane (row lane & 15 of tile lane >> 4), the
+// tokens' codes broadcast: 8 x (12 + 13 CNT) instructions and no idle columns, against about
+// 300 for the MMA form.
+template <bool L2, int CNT>
+__device__ __forceinline__ void stage_dp4a(float (&acc)[kDp4aTokens], uint32_t codes, const uint8_t* scales,
+                                           const uint8_t* const (&xb)[kDp4aTokens], const float* const (&db)[kDp4aTokens]) {
+    const int lane = threadIdx.x & 31, row = lane & 15;
+    const uint32_t base = codes + uint32_t(lane >> 4) * kTileBytes + uint32_t(row * 128);
+    const uint4 sc = *reinterpret_cast<const uint4*>(scales + lane * 16);
+    const uint32_t sw[4] = {sc.x, sc.y, sc.z, sc.w};
+    constexpr int AHEAD = CNT == 1 ? 4 : 2;  // blocks whose activations are fetched together
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            if (i >= nt) break;
-            const uint4* px = reinterpret_cast<const uint4*>(xq + rows.b[i] * pitch + q * 128 + c * 32);
-            const uint4 x0 = px[0], x1 = px[1];
-            const float4 d0 = *reinterpret_cast<const float4*>(xd + rows.s0[i] * spitch + q * 4);
-            const float4 d1 = *reinterpret_cast<const float4*>(xd + rows.s1[i] * spitch + q * 4);
-            const uint32_t bw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-            const float e0[4] = {d0.x, d0.y, d0.z, d0.w}, e1[4] = {d1.x, d1.y, d1.z, d1.w};
+    for (int b0 = 0; b0 < 8; b0 += AHEAD) {
+        uint4 x[CNT][2 * AHEAD];
+        float4 dx[CNT];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const unsigned long long dx = pack2(e0[b], e1[b]);
+        for (int t = 0; t < CNT; ++t) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    float f[4];
-                    mma_s8(f, a[b][m * 4], a[b][m * 4 + 1], a[b][m * 4 + 2], a[b][m * 4 + 3], bw[2 * b], bw[2 * b + 1]);
+            for (int i = 0; i < 2 * AHEAD; ++i) {  // word i % 4 of two blocks
+                const int b = b0 + i / 4 * 2;
+                x[t][i] = load_codes<L2>(xb[t] + (b >> 2) * 128 + (i & 3) * 32 + (b & 3) * 8);
+            }
+            dx[t] = load_scales<L2>(db[t] + (b0 & 4));
+        }
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float w = half_at(sw[m * 2 + r], q * 4 + b), n = __fmul_rn(-kMagic, w);  // exact
-                        const unsigned long long v = fma2(pack2(f[2 * r], f[2 * r + 1]), pack2(w, w), pack2(n, n));
-                        acc.v[i][m][r] = fma2(v, dx, acc.v[i][m][r]);
-                    }
+        for (int k0 = 0; k0 < AHEAD; k0 += 2) {
+            const int b = b0 + k0;
+            uint32_t w[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(w[k][0]), "=r"(w[k][1]), "=r"(w[k][2]), "=r"(w[k][3])
+                             : "r"(base + uint32_t(((b + k) ^ (row & 7)) << 4)));
+            const float2 dw = halves(sw[b >> 1]);
+#pragma unroll
+            for (int t = 0; t < CNT; ++t) {
+                int s0 = 0, s1 = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // words i of blocks b and b + 1: both K halves
+                    const uint4 v = x[t][2 * k0 + i];
+                    s0 = __dp4a(int(low_codes(w[0][i])), int(v.x), s0);
+                    s1 = __dp4a(int(low_codes(w[1][i])), int(v.z), s1);
+                    s0 = __dp4a(int(high_codes(w[0][i])), int(v.y), s0);
+                    s1 = __dp4a(int(high_codes(w[1][i])), int(v.w), s1);
                 }
+                acc[t] = fmaf(float(s0), __fmul_rn(dw.x, (b & 2) ? dx[t].z : dx[t].x), acc[t]);
+                acc[t] = fmaf(float(s1), __fmul_rn(dw.y, (b & 2) ? dx[t].w : dx[t].y), acc[t]);
             }
         }
     }
@@ -452,223 +560,303 @@ __device__ __forceinline__ Ring make_ring(uint8_t* smem, Ctrl* ctrl) {
     r.dead = false;
     return r;
 }
-__device__ __forceinline__ void init_ctrl(Ctrl* ctrl) {
+__device__ __forceinline__ void init_ctrl(Ctrl* ctrl, const CUtensorMap* tq, const CUtensorMap* ts) {
     if (threadIdx.x == 0) {
         for (int w = 0; w < kWarps; ++w)
             for (int s = 0; s < kStages; ++s) mbar_init(smem_addr(&ctrl->full[w][s]), 1);
         ctrl->abort = 0;
         mbar_init_fence();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(tq) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(ts) : "memory");
     }
 }
+
+// The activation rows a lane reads for a group: columns past the group repeat its last token
+// (a column never reaches another).
+struct Group {
+    int first, cnt;
+    int b, s0, s1;  // rows of columns lane/4, 2c, 2c+1; for dp4a s0, s1 are tokens 0 and 1
+    template <typename Map>
+    __device__ __forceinline__ void set(const Lists& l, int g, Map row) {
+        const int lane = threadIdx.x & 31;
+        first = l.from[g];
+        cnt = l.cnt[g];
+        const bool dp = cnt <= kDp4aTokens;
+        b = row(int(l.ord[first + min(lane >> 2, cnt - 1)]));
+        s0 = row(int(l.ord[first + (dp ? 0 : min(2 * (lane & 3), cnt - 1))]));
+        s1 = row(int(l.ord[first + (dp ? cnt - 1 : min(2 * (lane & 3) + 1, cnt - 1))]));
+    }
+};
+// Both forms' sums; the other one's stay zero.
+struct Sums {
+    unsigned long long m[2][2];
+    float d[kDp4aTokens];
+    __device__ __forceinline__ void clear() {
+        m[0][0] = m[0][1] = m[1][0] = m[1][1] = 0ull;
+        d[0] = d[1] = 0.0f;
+    }
+};
 
 // ------------------------------------------------------------------ gate, up and h
 constexpr int kRedPitch = 9;
 constexpr int kRedBytes = 4 * 64 * kRedPitch * 4;
-__host__ __device__ __forceinline__ size_t gate_up_smem(int E, int n, int group) {
-    return 1024 + kRingBytes + kCtrlBytes + kRedBytes + lists_bytes(E, n, group);
+__host__ __device__ __forceinline__ size_t gate_up_smem(int E, int n) {
+    return 1024 + kRingBytes + kCtrlBytes + kRedBytes + lists_bytes(E, n, kGroup);
 }
 
-// Items: (32 rows of I, group of tokens of one expert), dealt round-robin to the CTAs. Two warps share a
-// K slice's boxes (one per 16 gate and 16 up rows), four slices; their sums meet in shared
-// memory, where a warp per token forms h, its block's scale and codes. NT:
-// 8-token tiles of a group.
-template <int NT>
+// Items: (group of at most 8 tokens of one expert, 32 rows of I), dealt round-robin to the
+// CTAs. Two warps share a K slice's boxes (one per 16 gate and 16 up rows), four slices; their
+// sums meet in shared memory, where a warp per token forms h, its block's scale and codes.
 __global__ void __launch_bounds__(256, 2)
-    gate_up_kernel(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* xq, const float* xd,
-                   const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_s, int sc_tma,
-                   const uint16_t* __restrict__ wd, uint8_t* __restrict__ hq, float* __restrict__ hd) {
+    gate_up_kernel(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* xq,
+                   const float* xd, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_s,
+                   int sc_tma, const uint16_t* __restrict__ wd, uint8_t* __restrict__ hq, float* __restrict__ hd) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + kRingBytes);
     float* red = reinterpret_cast<float*>(smem + kRingBytes + kCtrlBytes);
     const int n = T * top_k;
-    const Lists l = lists_at(smem + kRingBytes + kCtrlBytes + kRedBytes, E, n, 8 * NT);
+    const Lists l = lists_at(smem + kRingBytes + kCtrlBytes + kRedBytes, smem, E, n, kGroup);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rg = warp & 1, ksl = warp >> 1;
-    init_ctrl(ctrl);
+    init_ctrl(ctrl, &tm_q, &tm_s);
     pdl_wait_primary();  // ids, xq and xd are written by the preceding kernel
     pdl_launch_dependents();
-    build_lists(l, ids, weights, n, top_k, E, 8 * NT);  // its barriers also publish the control block
+    build_lists(l, ids, weights, n, top_k, E, kGroup);
+    fence_proxy_async_smem();  // the lists' scratch lies in the ring, which TMA writes next
+    __syncthreads();
     const int B = H / 32, Bp = padded_blocks(H), nbox = Bp / kBoxBlocks;
     const int IB = I / 32, IBp = padded_blocks(I);
     const int nitems = *l.nact * IB;
     Ring ring = make_ring(smem, ctrl);
-    int pi = blockIdx.x, pj = ksl;  // the next box to fetch: item, box
-    auto row_of = [&](int item) { return int(l.act[item / IB]) * 2 * I + (item % IB) * 32 + rg * 16; };
+    // the next box to fetch: item, box, first gate row
+    int pi = blockIdx.x, pj = ksl, pr = 0;
+    auto row_of = [&](int item) {
+        const int gi = item / IB;
+        return int(l.act[gi]) * 2 * I + (item - gi * IB) * 32 + rg * 16;
+    };
+    const bool any = ksl < nbox;
+    if (any && pi < nitems) pr = row_of(pi);
     auto fetch = [&]() {
-        if (ksl >= nbox || pi >= nitems || ring.dead) return;
-        if (lane == 0) {
-            const int r = row_of(pi);
-            ring.issue(&tm_q, &tm_s, sc_tma, pj, r, r + I);
-        }
+        if (!any || pi >= nitems || ring.dead) return;
+        if (lane == 0) ring.issue(&tm_q, &tm_s, sc_tma, pj, pr, pr + I);
         ++ring.issued;
         pj += 4;
         if (pj >= nbox) {
             pj = ksl;
             pi += gridDim.x;
+            if (pi < nitems) pr = row_of(pi);
         }
     };
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) fetch();
+    fetch();
+    fetch();
 
     for (int item = blockIdx.x; item < nitems; item += gridDim.x) {
         const int gi = item / IB, ib = item - gi * IB;
-        const int first = l.from[gi], cnt = l.cnt[gi], nt = (cnt + 7) / 8;
-        const int r = row_of(item);
-        Rows<NT> rows;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            auto at = [&](int col) { return int(l.ord[first + min(i * 8 + col, cnt - 1)]) / top_k; };
-            rows.b[i] = at(lane >> 2);
-            rows.s0[i] = at(2 * (lane & 3));
-            rows.s1[i] = at(2 * (lane & 3) + 1);
-        }
-        Acc<NT> acc;
+        const int r = int(l.act[gi]) * 2 * I + ib * 32 + rg * 16;
+        Group gr;
+        gr.set(l, gi, [&](int slot) { return slot / top_k; });
+        const bool dp = gr.cnt <= kDp4aTokens;
+        const int pitch = Bp * 32;
+        const uint8_t* xb = xq + gr.b * pitch + (lane & 3) * 32;
+        const float *d0 = xd + gr.s0 * Bp, *d1 = xd + gr.s1 * Bp;
+        const uint8_t *t0 = xq + gr.s0 * pitch, *t1 = xq + gr.s1 * pitch;
+        Sums acc;
         acc.clear();
+#pragma unroll 1
         for (int j = ksl; j < nbox; j += 4) {
-            ring.wait(wd, sc_tma, j, r, r + I, B, &ctrl->abort);
             const int st = ring.used % kStages;
-            box_dots<NT>(acc, ring.codes + st * kStageBytes, ring.scales + st * kScaleBytes, xq + j * 256,
-                         xd + j * kBoxBlocks, Bp * 32, Bp, rows, nt);
+            const uint32_t cq = ring.codes + st * kStageBytes;
+            const uint8_t* cs = ring.scales + st * kScaleBytes;
+            if (dp) {
+                ring.wait(wd, sc_tma, j, r, r + I, B, &ctrl->abort);
+                const uint8_t* const x[2] = {t0 + j * 256, t1 + j * 256};
+                const float* const d[2] = {d0 + j * 8, d1 + j * 8};
+                if (gr.cnt == 1)
+                    stage_dp4a<false, 1>(acc.d, cq, cs, x, d);
+                else
+                    stage_dp4a<false, 2>(acc.d, cq, cs, x, d);
+            } else {
+                const Frag f = load_frag<false>(xb + j * 256, d0 + j * 8, d1 + j * 8);
+                ring.wait(wd, sc_tma, j, r, r + I, B, &ctrl->abort);
+                stage_mma(acc.m, cq, cs, f);
+            }
             __syncwarp();
             ++ring.used;
             fetch();
         }
+        float* p = red + ksl * 64 * kRedPitch;
+        if (dp) {
+            float* q = p + ((lane >> 4) * 32 + rg * 16 + (lane & 15)) * kRedPitch;
+            q[0] = acc.d[0];
+            q[1] = acc.d[1];
+        } else {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            if (i >= nt) break;
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float a, b;
-                    unpack2(acc.v[i][m][h], a, b);
-                    float* p = red + (ksl * 64 + m * 32 + rg * 16 + h * 8 + (lane >> 2)) * kRedPitch + 2 * (lane & 3);
-                    p[0] = a;
-                    p[1] = b;
-                }
-            __syncthreads();
-            if (i * 8 + warp < cnt) {
-                const int slot = l.ord[first + i * 8 + warp];
-                float gate = 0.0f, up = 0.0f;
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    gate = __fadd_rn(gate, red[(s * 64 + lane) * kRedPitch + warp]);
-                    up = __fadd_rn(up, red[(s * 64 + 32 + lane) * kRedPitch + warp]);
-                }
-                const float hv = __fmul_rn(__fdiv_rn(gate, 1.0f + expf(-gate)), up);
-                float amax = fabsf(hv);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const float d = __fdiv_rn(amax, 127.0f);
-                const float id = d != 0.0f ? __frcp_rn(d) : 0.0f;
-                const int code = max(-127, min(127, int(roundf(__fmul_rn(hv, id)))));
-                uint32_t w = (uint32_t(code) & 0xFFu) << (8 * (lane & 3));
-                w |= __shfl_xor_sync(0xffffffffu, w, 1);
-                w |= __shfl_xor_sync(0xffffffffu, w, 2);
-                if ((lane & 3) == 0)
-                    *reinterpret_cast<uint32_t*>(hq + int64_t(slot) * IBp * 32 + word_offset(ib, lane >> 2)) = w;
-                if (lane == 0) hd[int64_t(slot) * IBp + ib] = __fmul_rn(d, 0.0625f);
-                if (ib == IB - 1 && lane < IBp - IB) hd[int64_t(slot) * IBp + IB + lane] = 0.0f;  // the padding
+            for (int m = 0; m < 4; ++m) {
+                float a, b;
+                unpack2(acc.m[m >> 1][m & 1], a, b);
+                float* q = p + ((m >> 1) * 32 + rg * 16 + (m & 1) * 8 + (lane >> 2)) * kRedPitch + 2 * (lane & 3);
+                q[0] = a;
+                q[1] = b;
             }
-            __syncthreads();
         }
+        __syncthreads();
+        if (warp < gr.cnt) {
+            const int slot = l.ord[gr.first + warp];
+            float gate = 0.0f, up = 0.0f;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                gate = __fadd_rn(gate, red[(s * 64 + lane) * kRedPitch + warp]);
+                up = __fadd_rn(up, red[(s * 64 + 32 + lane) * kRedPitch + warp]);
+            }
+            const float hv = __fmul_rn(__fdiv_rn(gate, 1.0f + expf(-gate)), up);
+            float amax = fabsf(hv);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const float d = __fdiv_rn(amax, 127.0f);
+            const float id = d != 0.0f ? __frcp_rn(d) : 0.0f;
+            const int code = max(-127, min(127, int(roundf(__fmul_rn(hv, id)))));
+            uint32_t w = (uint32_t(code) & 0xFFu) << (8 * (lane & 3));
+            w |= __shfl_xor_sync(0xffffffffu, w, 1);
+            w |= __shfl_xor_sync(0xffffffffu, w, 2);
+            if ((lane & 3) == 0)
+                *reinterpret_cast<uint32_t*>(hq + int64_t(slot) * IBp * 32 + word_offset(ib, lane >> 2)) = w;
+            if (lane == 0) hd[int64_t(slot) * IBp + ib] = __fmul_rn(d, 0.0625f);
+            if (ib == IB - 1 && lane < IBp - IB) hd[int64_t(slot) * IBp + IB + lane] = 0.0f;  // the padding
+        }
+        __syncthreads();
     }
     ring.drain();
 }
 
 // ------------------------------------------------------------------ down and the weighted sum
+constexpr int kDownTokens = 32;  // tokens of one CTA: the warps' sums take 1 KB of shared memory each
 constexpr int kYPitch = 33;
-__host__ __device__ __forceinline__ size_t down_smem(int T, int E, int n, int group) {
-    return 1024 + kRingBytes + kCtrlBytes + size_t(kWarps) * T * kYPitch * 4 + lists_bytes(E, n, group);
+__host__ __device__ __forceinline__ size_t down_smem(int T, int E, int n) {
+    return 1024 + kRingBytes + kCtrlBytes + size_t(kWarps) * T * kYPitch * 4 + lists_bytes(E, n, kGroup);
 }
 
-// Grid: x = split (the cluster), y = 32 rows of H. The boxes of all used experts for those
-// rows are dealt round-robin to the warps of the cluster; each warp adds its sums, times the
-// slots' weights, to a [token][row] array of its own, and the arrays are added in a fixed
-// order (within the CTA, then across the cluster through distributed shared memory).
-template <int NT>
+// Grid: x = split (the cluster), y = 32 rows of H, z = 32 tokens. The boxes of all used experts
+// for those rows are dealt round-robin to the warps of the cluster; each warp adds its sums,
+// times the slots' weights, to a [token][row] array of its own, and the arrays are added in a
+// fixed order (within the CTA, then across the cluster through distributed shared memory).
 __global__ void __launch_bounds__(256, 2)
-    down_kernel(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* hq,
+    down_kernel(int Tall, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* hq,
                 const float* hd, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_s,
                 int sc_tma, const uint16_t* __restrict__ wd, void* __restrict__ y, int out_bf16) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + kRingBytes);
     float* ybuf = reinterpret_cast<float*>(smem + kRingBytes + kCtrlBytes);
+    // this CTA's tokens: ids, weights and h start at its first slot
+    const int tok0 = blockIdx.z * kDownTokens, T = min(kDownTokens, Tall - tok0);
     const int n = T * top_k, YT = T * kYPitch;
-    const Lists l = lists_at(reinterpret_cast<uint8_t*>(ybuf + kWarps * YT), E, n, 8 * NT);
+    const int B = I / 32, Bp = padded_blocks(I), nbox = Bp / kBoxBlocks, pitch = Bp * 32;
+    ids += tok0 * top_k;
+    weights += tok0 * top_k;
+    hq += int64_t(tok0) * top_k * pitch;
+    hd += int64_t(tok0) * top_k * Bp;
+    const Lists l = lists_at(reinterpret_cast<uint8_t*>(ybuf + kWarps * YT), smem, E, n, kGroup);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n0 = blockIdx.y * 32, slices = gridDim.x * kWarps;
-    init_ctrl(ctrl);
+    init_ctrl(ctrl, &tm_q, &tm_s);
     for (int i = threadIdx.x; i < kWarps * YT; i += 256) ybuf[i] = 0.0f;
     // Read before the wait: ids and weights come from the kernel before the preceding one,
     // which has completed, since every CTA of the preceding kernel waits for it before it
     // lets this grid start (and the loads are from L2).
-    build_lists(l, ids, weights, n, top_k, E, 8 * NT);
-    const int B = I / 32, Bp = padded_blocks(I), nbox = Bp / kBoxBlocks;
-    const int nchunks = *l.nact * nbox;
+    build_lists(l, ids, weights, n, top_k, E, kGroup);
+    fence_proxy_async_smem();
+    __syncthreads();
+    const int nact = *l.nact;
     Ring ring = make_ring(smem, ctrl);
-    int pc = blockIdx.x * kWarps + warp;
+    auto step = [&](int& g, int& j, int by) {
+        j += by;
+        while (j >= nbox) {
+            j -= nbox;
+            ++g;
+        }
+    };
+    int pg = 0, pj = 0;  // the next box to fetch: group, box
+    step(pg, pj, blockIdx.x * kWarps + warp);
     auto fetch = [&]() {
-        if (pc >= nchunks || ring.dead) return;
+        if (pg >= nact || ring.dead) return;
         if (lane == 0) {
-            const int r = int(l.act[pc / nbox]) * H + n0;
-            ring.issue(&tm_q, &tm_s, sc_tma, pc % nbox, r, r + 16);
+            const int r = int(l.act[pg]) * H + n0;
+            ring.issue(&tm_q, &tm_s, sc_tma, pj, r, r + 16);
         }
         ++ring.issued;
-        pc += slices;
+        step(pg, pj, slices);
     };
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) fetch();
+    int ug = pg, uj = pj;  // the box in hand
+    fetch();
+    fetch();
     pdl_wait_primary();  // hq and hd
 
     float* yw = ybuf + warp * YT;
-    Acc<NT> acc;
-    Rows<NT> rows;
-    int a = -1, first = 0, cnt = 0, nt = 0;
+    Sums acc;
+    Group gr;
+    gr.cnt = 0;
+    int a = -1;
     auto flush = [&]() {
+        if (gr.cnt <= kDp4aTokens) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            if (i >= nt) break;
+            for (int t = 0; t < kDp4aTokens; ++t)
+                if (t < gr.cnt) {
+                    const int slot = l.ord[gr.first + t];
+                    float* p = yw + slot / top_k * kYPitch + lane;
+                    *p = fmaf(l.w[slot], acc.d[t], *p);
+                }
+        } else {
 #pragma unroll
             for (int col = 0; col < 2; ++col) {
-                const int at = i * 8 + 2 * (lane & 3) + col;
-                if (at >= cnt) continue;
-                const int slot = l.ord[first + at];
+                const int at = 2 * (lane & 3) + col;
+                if (at >= gr.cnt) continue;
+                const int slot = l.ord[gr.first + at];
                 const float w = l.w[slot];
                 float* p = yw + slot / top_k * kYPitch + (lane >> 2);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     float v0, v1;
-                    unpack2(acc.v[i][m >> 1][m & 1], v0, v1);
+                    unpack2(acc.m[m >> 1][m & 1], v0, v1);
                     p[m * 8] = fmaf(w, col ? v1 : v0, p[m * 8]);
                 }
             }
         }
+        __syncwarp();
     };
-    for (int c = blockIdx.x * kWarps + warp; c < nchunks; c += slices) {
-        const int an = c / nbox, j = c - an * nbox;
-        if (an != a) {
+    const uint8_t *xb = hq, *t0 = hq, *t1 = hq;
+    const float *d0 = hd, *d1 = hd;
+#pragma unroll 1
+    while (ug < nact) {
+        if (ug != a) {
             if (a >= 0) flush();
-            a = an;
-            first = l.from[a];
-            cnt = l.cnt[a];
-            nt = (cnt + 7) / 8;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                auto at = [&](int col) { return int(l.ord[first + min(i * 8 + col, cnt - 1)]); };
-                rows.b[i] = at(lane >> 2);
-                rows.s0[i] = at(2 * (lane & 3));
-                rows.s1[i] = at(2 * (lane & 3) + 1);
-            }
+            a = ug;
+            gr.set(l, a, [](int slot) { return slot; });
+            xb = hq + int64_t(gr.b) * pitch + (lane & 3) * 32;
+            t0 = hq + int64_t(gr.s0) * pitch;
+            t1 = hq + int64_t(gr.s1) * pitch;
+            d0 = hd + int64_t(gr.s0) * Bp;
+            d1 = hd + int64_t(gr.s1) * Bp;
             acc.clear();
         }
-        const int r = int(l.act[a]) * H + n0;
-        ring.wait(wd, sc_tma, j, r, r + 16, B, &ctrl->abort);
+        const int r = int(l.act[ug]) * H + n0, j = uj;
+        step(ug, uj, slices);
         const int st = ring.used % kStages;
-        box_dots<NT>(acc, ring.codes + st * kStageBytes, ring.scales + st * kScaleBytes, hq + j * 256,
-                     hd + j * kBoxBlocks, Bp * 32, Bp, rows, nt);
+        const uint32_t cq = ring.codes + st * kStageBytes;
+        const uint8_t* cs = ring.scales + st * kScaleBytes;
+        if (gr.cnt <= kDp4aTokens) {
+            ring.wait(wd, sc_tma, j, r, r + 16, B, &ctrl->abort);
+            const uint8_t* const x[2] = {t0 + j * 256, t1 + j * 256};
+            const float* const d[2] = {d0 + j * 8, d1 + j * 8};
+            if (gr.cnt == 1)
+                stage_dp4a<true, 1>(acc.d, cq, cs, x, d);
+            else
+                stage_dp4a<true, 2>(acc.d, cq, cs, x, d);
+        } else {
+            const Frag f = load_frag<true>(xb + j * 256, d0 + j * 8, d1 + j * 8);
+            ring.wait(wd, sc_tma, j, r, r + 16, B, &ctrl->abort);
+            stage_mma(acc.m, cq, cs, f);
+        }
         __syncwarp();
         ++ring.used;
         fetch();
@@ -688,7 +876,7 @@ __global__ void __launch_bounds__(256, 2)
         cluster_sync();
     else
         __syncthreads();
-    if (!ctrl->abort) {
+    if (!*reinterpret_cast<volatile uint32_t*>(&ctrl->abort)) {
         for (int i = blockIdx.x * 256 + threadIdx.x; i < T * 32; i += cs * 256) {
             const uint32_t p = smem_addr(ybuf + (i >> 5) * kYPitch + (i & 31));
             float v = 0.0f;
@@ -697,7 +885,7 @@ __global__ void __launch_bounds__(256, 2)
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(mapa_shared(p, z)));
                 v = __fadd_rn(v, u);
             }
-            const int64_t o = int64_t(i >> 5) * H + n0 + (i & 31);
+            const int64_t o = int64_t(tok0 + (i >> 5)) * H + n0 + (i & 31);
             if (out_bf16)
                 reinterpret_cast<__nv_bfloat16*>(y)[o] = __float2bfloat16_rn(v);
             else

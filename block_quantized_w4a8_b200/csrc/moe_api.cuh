@@ -90,35 +90,35 @@ bool moe_maps(CUtensorMap* tq, CUtensorMap* ts, int* sc_tma, const uint8_t* q, c
                                   uint64_t(K / 32) * 2, 8, 16));
 }
 
-template <int NT>
-w4a8_status launch_experts(int T, int E, int H, int I, int top_k, const int* ids, const float* weights,
-                           const uint8_t* gq, const uint16_t* gd, const uint8_t* dq, const uint16_t* dd, int out_bf16,
-                           void* y, const MoeWs& w, cudaStream_t stream) {
+w4a8_status run_experts(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* gq,
+                        const uint16_t* gd, const uint8_t* dq, const uint16_t* dd, w4a8_dtype odt, void* y,
+                        const MoeWs& w, cudaStream_t stream) {
     CUtensorMap gtq, gts, dtq, dts;
     int gsc, dsc;
     if (!moe_maps(&gtq, &gts, &gsc, gq, gd, int64_t(E) * 2 * I, H) ||
         !moe_maps(&dtq, &dts, &dsc, dq, dd, int64_t(E) * H, I))
         return W4A8_ERR_CUDA;
-    const int n = T * top_k, group = 8 * NT;
-    const size_t gs = moe::gate_up_smem(E, n, group), ds = moe::down_smem(T, E, n, group);
     // limits for the largest lists, so that one setting serves every call
-    constexpr int kT = NT == 1 ? 8 : moe::kMaxTokens;
-    cudaError_t e = smem_limit_once(moe::gate_up_kernel<NT>,
-                                    int(moe::gate_up_smem(moe::kMaxExperts, kT * moe::kMaxTopK, group)));
+    const int n = T * top_k, td = T < moe::kDownTokens ? T : moe::kDownTokens;
+    cudaError_t e = smem_limit_once(moe::gate_up_kernel,
+                                    int(moe::gate_up_smem(moe::kMaxExperts, moe::kMaxTokens * moe::kMaxTopK)));
     if (e == cudaSuccess)
-        e = smem_limit_once(moe::down_kernel<NT>, int(moe::down_smem(kT, moe::kMaxExperts, kT * moe::kMaxTopK, group)));
+        e = smem_limit_once(moe::down_kernel, int(moe::down_smem(moe::kDownTokens, moe::kMaxExperts,
+                                                                 moe::kDownTokens * moe::kMaxTopK)));
     if (e != cudaSuccess) return cuda_status(e);
-    const int64_t items = int64_t(moe::max_groups(E, n, group)) * (I / 32);
+    const int64_t items = int64_t(moe::max_groups(E, n, moe::kGroup)) * (I / 32);
     const int64_t slots = int64_t(sm_count()) * 2;
-    e = launch_pdl(moe::gate_up_kernel<NT>, dim3(unsigned(items < slots ? items : slots)), dim3(256), gs, stream, T, E,
-                   H, I, top_k, ids, weights, (const uint8_t*)w.xq, (const float*)w.xd, gtq, gts, gsc, gd, w.hq, w.hd);
+    e = launch_pdl(moe::gate_up_kernel, dim3(unsigned(items < slots ? items : slots)), dim3(256),
+                   moe::gate_up_smem(E, n), stream, T, E, H, I, top_k, ids, weights, (const uint8_t*)w.xq,
+                   (const float*)w.xd, gtq, gts, gsc, gd, w.hq, w.hd);
     if (e != cudaSuccess) return cuda_status(e);
+    const int tz = int(cdiv(T, moe::kDownTokens));
     int cs = 8;  // the largest cluster whose grid is resident at once
-    while (cs > 1 && int64_t(H / 32) * cs > slots) cs >>= 1;
+    while (cs > 1 && int64_t(H / 32) * tz * cs > slots) cs >>= 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(cs), unsigned(H / 32));
+    cfg.gridDim = dim3(unsigned(cs), unsigned(H / 32), unsigned(tz));
     cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = ds;
+    cfg.dynamicSmemBytes = moe::down_smem(td, E, td * top_k);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -129,16 +129,9 @@ w4a8_status launch_experts(int T, int E, int H, int I, int top_k, const int* ids
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cuda_status(cudaLaunchKernelEx(&cfg, moe::down_kernel<NT>, T, E, H, I, top_k, ids, weights,
-                                          (const uint8_t*)w.hq, (const float*)w.hd, dtq, dts, dsc, dd, y, out_bf16));
-}
-
-w4a8_status run_experts(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* gq,
-                        const uint16_t* gd, const uint8_t* dq, const uint16_t* dd, w4a8_dtype odt, void* y,
-                        const MoeWs& w, cudaStream_t stream) {
-    const int bf = odt == W4A8_BF16 ? 1 : 0;
-    if (T <= 8) return launch_experts<1>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
-    return launch_experts<2>(T, E, H, I, top_k, ids, weights, gq, gd, dq, dd, bf, y, w, stream);
+    return cuda_status(cudaLaunchKernelEx(&cfg, moe::down_kernel, T, E, H, I, top_k, ids, weights,
+                                          (const uint8_t*)w.hq, (const float*)w.hd, dtq, dts, dsc, dd, y,
+                                          odt == W4A8_BF16 ? 1 : 0));
 }
 
 }  // namespace
