@@ -60,8 +60,38 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 }
 __device__ __forceinline__ void tmem_load(uint32_t t, uint32_t (&r)[16]) { tmem_ld_32x32_x16(t, r); }
 __device__ __forceinline__ void tmem_load(uint32_t t, uint32_t (&r)[32]) { tmem_ld_32x32(t, r); }
+__device__ __forceinline__ void tmem_load(uint32_t t, uint32_t (&r)[64]) { tmem_ld_32x32_x64(t, r); }
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[64]) { tmem_wait_ld64(r); }
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) { tmem_wait_ld16(r); }
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) { tmem_wait_ld(r); }
+
+// bounded_wait_warp without a call: the register split of the CTA-pair kernel (setmaxnreg) rules
+// out calls.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait_nohint<CLUSTER>(bar, parity)), 1)) return true;
+    const unsigned long long t0 = global_timer_ns();
+#pragma unroll 1
+    for (uint32_t it = 1;; ++it) {
+        if (__all_sync(0xffffffffu, mbar_try_wait<CLUSTER>(bar, parity))) return true;
+        if ((it & 15u) == 0u) {
+            const bool late = global_timer_ns() - t0 > kWaitLimitNs;
+            if (late && (threadIdx.x & 31u) == 0u) {
+                atomicOr(&g_device_status, kDevErrTimeout);
+                *abort = 1u;
+            }
+            if (__any_sync(0xffffffffu, late || *abort != 0u)) return false;
+        }
+    }
+}
+
+// drain_wait_warp without a call.
+__device__ __forceinline__ void drain_inline(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+    const unsigned long long t0 = global_timer_ns();
+#pragma unroll 1
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        if (__any_sync(0xffffffffu, global_timer_ns() - t0 > limit_ns)) return;
+}
 
 constexpr int kMaxStages = 8;
 constexpr int kMaxBufs = 8;
@@ -282,24 +312,31 @@ __global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
 // CTA pairs (cta_group::2), persistent: tiles of 256 tokens x 256 output columns, each CTA
 // holding 128 tokens (its TMEM lanes) and staging half of the weight tile. Two tensor-memory
 // tiles of 256 columns alternate, so the MMAs of the next block run while the epilogue adds
-// the last one; the output of a tile is stored while the next tile's first blocks run.
+// the last one; the output of a tile is stored while the next tile's first blocks run. A stage
+// is handed back by its MMAs' commit, not by the epilogue, which takes the token scales from
+// global memory a block ahead.
 struct PairGeo {
     static constexpr int STAGE = 2 * kTile;  // token tile, weight half
     static constexpr int NS = 6;
     static constexpr int NBUF = 2;
     static constexpr int CW = 128;           // columns per epilogue warp
-    static constexpr int LD = 32;
-    static constexpr int EPI_WARPS = 8;
+    static constexpr int LD = 64;            // columns per tensor-memory load
+    static constexpr int EPI_WARPS = 8;      // two warpgroups
     static constexpr int COPY_WARP = 8, MMA_WARP = 9;
-    static constexpr int THREADS = 320;
-    static constexpr int OFF_SX = NS * STAGE;
-    static constexpr int OFF_CTRL = OFF_SX + NS * 128 * 4;
+    static constexpr int THREADS = 384;
+    // Registers: launched with 168 per thread (three warpgroups on 64 K registers); the third
+    // warpgroup keeps 40, the epilogue takes 232 each for 128 accumulators and a piece of 64
+    // columns: 2 * 232 + 40 = 3 * 168. Measured on the gradient of 1024 x 4096 x 4096 (whole
+    // call): 30.2 us; pieces of 32 columns, which spill in the loop, 40.9; sixteen warps of 64
+    // columns 35.3.
+    static constexpr int OFF_STG = NS * STAGE;
+    static constexpr int OFF_CTRL = OFF_STG + EPI_WARPS * 32 * 32 * 4;
     static constexpr int SMEM = OFF_CTRL + 512 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
 };
 struct PairCtrl {
     unsigned long long full[kMaxStages];    // this CTA's copies (1 arrival + bytes)
-    unsigned long long empty[kMaxStages];   // one arrival per epilogue warp of this CTA
+    unsigned long long empty[kMaxStages];   // pair commit of the stage's MMAs, on both CTAs
     unsigned long long pfull[kMaxStages];   // even CTA: the odd CTA's stage is ready
     unsigned long long tfull[2];            // pair commit, on both CTAs
     unsigned long long tempty[2];           // even CTA: one arrival per epilogue warp of both
@@ -319,34 +356,74 @@ __device__ __forceinline__ void pair_tile(int t, int tm, int tc, int& mt, int& c
     ct = band * BAND + in - mt * w;
 }
 
-// y[row .. row+7] of columns n .. n+7 (row a multiple of 8 elements).
-__device__ __forceinline__ void epi_store8(void* y, int64_t idx, int n, const float* v, const Epilogue& e) {
-    if (e.out_bf16) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(epi_value(e, n + 2 * i, v[2 * i]), epi_value(e, n + 2 * i + 1, v[2 * i + 1]));
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// A warp's 32 x 32 f32 staging area: word c of row r at r * 32 + (c ^ 2 (r & 15)), so that both the
+// writes (a row per lane, two words at a time) and the reads (a row per half-warp) touch
+// every bank once.
+__device__ __forceinline__ uint32_t stage_word(int r, int c) { return uint32_t(r * 32 + (c ^ ((r & 15) * 2))); }
+
+// The staged piece to rows m0.. and columns c0.. of the output (M x C), with the epilogue: two
+// columns per lane, two rows per store.
+__device__ __forceinline__ void store_piece(void* out, const float* stg, int m0, int M, int c0, int C, const Epilogue& epi) {
+    const int lane = threadIdx.x & 31, cc = (lane & 15) * 2, c = c0 + cc;
+    if (c >= C) return;
+    const int rows = min(32, M - m0);
+    const bool two = c + 1 < C, wide = (C & 1) == 0;
+    const bool bias = epi.bias != nullptr;
+    const float b0 = epi_value(epi, c, 0.0f), b1 = two ? epi_value(epi, c + 1, 0.0f) : 0.0f;
+#pragma unroll 8
+    for (int i = lane >> 4; i < rows; i += 2) {
+        float2 v = *reinterpret_cast<const float2*>(stg + stage_word(i, cc));
+        if (bias) {
+            v.x = __fadd_rn(v.x, b0);
+            v.y = __fadd_rn(v.y, b1);
         }
-        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(y) + idx) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-        epi_store4(y, idx, n, v[0], v[1], v[2], v[3], e);
-        epi_store4(y, idx + 4, n + 4, v[4], v[5], v[6], v[7], e);
+        const int64_t o = int64_t(m0 + i) * C + c;
+        if (epi.out_bf16) {
+            __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(out) + o;
+            const __nv_bfloat162 w = __floats2bfloat162_rn(v.x, v.y);
+            if (wide) {
+                *reinterpret_cast<__nv_bfloat162*>(p) = w;
+            } else {
+                p[0] = w.x;
+                if (two) p[1] = w.y;
+            }
+        } else {
+            float* p = reinterpret_cast<float*>(out) + o;
+            if (wide) {
+                *reinterpret_cast<float2*>(p) = v;
+            } else {
+                p[0] = v.x;
+                if (two) p[1] = v.y;
+            }
+        }
     }
+}
+
+// Loads that stay where they are written (a plain __ldg may be moved down to its use).
+__device__ __forceinline__ float load_ahead(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
 }
 
 template <bool TRANS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
     gemm_pair_fp8_kernel(int M, int C, int R, const __grid_constant__ CUtensorMap tm_w,
-                         const __grid_constant__ CUtensorMap tm_x, const float* __restrict__ sx, int spitch,
+                         const __grid_constant__ CUtensorMap tm_x, const float* sx, int spitch,
                          const float* __restrict__ sw, int swcols, int tiles_m, int tiles_c, void* __restrict__ out,
                          Epilogue epi) {
+    
     using G = PairGeo;
     constexpr int NS = G::NS, NBUF = G::NBUF, CW = G::CW, LD = G::LD;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     PairCtrl* ctrl = reinterpret_cast<PairCtrl*>(smem + G::OFF_CTRL);
-    float* ssx = reinterpret_cast<float*>(smem + G::OFF_SX);
     volatile uint32_t* abort = &ctrl->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -358,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(bar(&ctrl->full[s]), 1);
-            mbar_init(bar(&ctrl->empty[s]), G::EPI_WARPS);
+            mbar_init(bar(&ctrl->empty[s]), 1);
             mbar_init(bar(&ctrl->pfull[s]), 1);
         }
         for (int j = 0; j < NBUF; ++j) {
@@ -379,10 +456,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
     const uint32_t tmem_base = ctrl->tmem_base;
     pdl_launch_dependents();
     const uint32_t smem0 = smem_addr(smem);
+     pdl_wait_primary();  // the token operand and its scales are written by the preceding kernel
 
+    if (warp >= G::COPY_WARP) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == G::COPY_WARP) {
         const bool leader = elect_one();
-        pdl_wait_primary();  // the token operand is written by the preceding kernel
         int it = 0;
         bool go = true;
         for (int t = pair; t < ntiles && go; t += npairs) {
@@ -391,22 +469,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
             const int m0 = mt * 256 + int(rank) * 128, c0 = ct * 256 + int(rank) * 128;
             for (int b = 0; b < nblk; ++b, ++it) {
                 const int slot = it % NS;
-                if (!bounded_wait_warp(bar(&ctrl->empty[slot]), ((it / NS) & 1) ^ 1, abort)) {
+                if (!wait_inline<true>(bar(&ctrl->empty[slot]), ((it / NS) & 1) ^ 1, abort)) {
                     go = false;
                     break;
                 }
                 if (leader) {
                     const uint32_t fb = bar(&ctrl->full[slot]);
-                    mbar_arrive_expect_tx(fb, uint32_t(G::STAGE + 512));
+                    mbar_arrive_expect_tx(fb, uint32_t(G::STAGE));
                     const uint32_t st = smem0 + slot * G::STAGE;
                     tma_load_2d<1>(st, &tm_x, b * kBlk, m0, fb);
                     tma_load_2d<1>(st + kTile, &tm_w, TRANS ? c0 : b * kBlk, TRANS ? b * kBlk : c0, fb);
-                    bulk_g2s(smem_addr(ssx + slot * 128), sx + int64_t(b) * spitch + m0, 512, fb);
                 }
                 __syncwarp();
             }
         }
-        for (int i = max(0, it - NS); i < it; ++i) drain_wait_warp(bar(&ctrl->full[i % NS]), (i / NS) & 1, 200000ull);
+        for (int i = max(0, it - NS); i < it; ++i) drain_inline(bar(&ctrl->full[i % NS]), (i / NS) & 1, 200000ull);
     } else if (warp == G::MMA_WARP) {
         const bool leader = elect_one();
         uint32_t local_abort = 0;
@@ -416,9 +493,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
             constexpr uint32_t idesc = idesc_e4m3(256, 256, false, TRANS);
             for (int it = 0; it < total; ++it) {
                 const int slot = it % NS, buf = it % NBUF;
-                if (!bounded_wait_warp(bar(&ctrl->full[slot]), (it / NS) & 1, abort)) break;
-                if (!bounded_wait_warp<true>(bar(&ctrl->pfull[slot]), (it / NS) & 1, abort)) break;
-                if (!bounded_wait_warp<true>(bar(&ctrl->tempty[buf]), ((it / NBUF) & 1) ^ 1, abort)) break;
+                if (!wait_inline<false>(bar(&ctrl->full[slot]), (it / NS) & 1, abort)) break;
+                if (!wait_inline<true>(bar(&ctrl->pfull[slot]), (it / NS) & 1, abort)) break;
+                if (!wait_inline<true>(bar(&ctrl->tempty[buf]), ((it / NBUF) & 1) ^ 1, abort)) break;
                 tc_fence_after();
                 if (leader) {
                     const uint32_t x = smem0 + slot * G::STAGE, w = x + kTile;
@@ -427,6 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
                         mma_f8_pair(tmem_base + buf * 256, desc_sw128(x + k_offset<false>(kk)),
                                     desc_sw128(w + k_offset<TRANS>(kk)), idesc, kk != 0);
                     tc_commit_pair(bar(&ctrl->tfull[buf]), 3);
+                    tc_commit_pair(bar(&ctrl->empty[slot]), 3);
                 }
                 __syncwarp();
             }
@@ -434,51 +512,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
         } else {
             const uint32_t pfull0 = mapa_shared(bar(&ctrl->pfull[0]), 0);
             for (int it = 0; it < total; ++it) {
-                if (!bounded_wait_warp(bar(&ctrl->full[it % NS]), (it / NS) & 1, abort)) break;
+                if (!wait_inline<false>(bar(&ctrl->full[it % NS]), (it / NS) & 1, abort)) break;
                 if (leader) mbar_arrive_remote(pfull0 + uint32_t(it % NS) * 8u);
                 __syncwarp();
             }
         }
         __syncwarp();
-        bounded_wait_warp(bar(&ctrl->drain), 0, &local_abort);
-    } else {
-        const int q = warp & 3, half = warp >> 2;
-        const int r = q * 32 + lane;  // this thread's token within the CTA's 128
-        const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16) + half * CW;
+        wait_inline<false>(bar(&ctrl->drain), 0, &local_abort);
+    } else if (warp < G::EPI_WARPS) {
+        const int q = warp & 3, cg = warp >> 2;  // TMEM lane quarter, half of the columns
+        const int r = q * 32 + lane;             // this thread's token within the CTA's 128
+        const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16) + cg * CW;
         const uint32_t tempty0 = rank == 0 ? bar(&ctrl->tempty[0]) : mapa_shared(bar(&ctrl->tempty[0]), 0);
-        float acc[CW];
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        unsigned long long acc[CW / 2];
         int it = 0;
         bool go = true;
         for (int t = pair; t < ntiles && go; t += npairs) {
             int mt, ct;
             pair_tile(t, tiles_m, tiles_c, mt, ct);
-            const int cb = ct * 2 + half;  // weight scale column of this warp
+            const int m = mt * 256 + int(rank) * 128 + r;
+            const int cb = ct * 2 + cg;  // weight scale column of this warp
             const bool inside = cb * 128 < C;
             const float* swp = TRANS ? sw + cb : sw + int64_t(cb) * swcols;
             const int64_t swstep = TRANS ? swcols : 1;
+            const float* sxp = sx + m;  // the scales' rows are padded to whole tiles
 #pragma unroll
-            for (int j = 0; j < CW; ++j) acc[j] = 0.0f;
-            float wnext = inside ? __ldg(swp) : 0.0f;
+            for (int j = 0; j < CW / 2; ++j) acc[j] = 0ull;
+            float wnext = inside ? load_ahead(swp) : 0.0f, snext = load_ahead(sxp);
+#pragma unroll 1
             for (int b = 0; b < nblk; ++b, ++it) {
-                const int slot = it % NS, buf = it % NBUF;
-                const float w = wnext;
-                if (inside && b + 1 < nblk) wnext = __ldg(swp + (b + 1) * swstep);
-                if (!bounded_wait_warp<true>(bar(&ctrl->tfull[buf]), (it / NBUF) & 1, abort) ||
-                    !bounded_wait_warp(bar(&ctrl->full[slot]), (it / NS) & 1, abort)) {  // the scales' copy
+                const int buf = it % NBUF;
+                const float f = __fmul_rn(snext, wnext);
+                if (b + 1 < nblk) {
+                    sxp += spitch;
+                    snext = load_ahead(sxp);
+                    swp += swstep;
+                    if (inside) wnext = load_ahead(swp);
+                }
+                const unsigned long long f2 = pack2(f, f);
+                if (!wait_inline<true>(bar(&ctrl->tfull[buf]), (it / NBUF) & 1, abort)) {
                     go = false;
                     break;
                 }
+                  
                 tc_fence_after();
-                const float s = ssx[slot * 128 + r];
-                __syncwarp();
-                if (lane == 0) mbar_arrive_after(bar(&ctrl->empty[slot]), s);
-                const float f = __fmul_rn(s, w);
 #pragma unroll
-                for (int h = 0; h < CW; h += LD) {
+                for (int h = 0; h < CW / LD; ++h) {
                     uint32_t p[LD];
-                    tmem_load(lane_base + buf * 256 + h, p);
+                    tmem_load(lane_base + buf * 256 + h * LD, p);
                     tmem_wait(p);
-                    if (h + LD == CW) {
+                    if (h + 1 == CW / LD) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
@@ -489,25 +573,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
                         }
                     }
 #pragma unroll
-                    for (int j = 0; j < LD; ++j) acc[h + j] = fmaf(__uint_as_float(p[j]), f, acc[h + j]);
+                    for (int j = 0; j < LD / 2; ++j)
+                        acc[h * LD / 2 + j] = fma2(pack2(__uint_as_float(p[2 * j]), __uint_as_float(p[2 * j + 1])),
+                                                   f2, acc[h * LD / 2 + j]);
                 }
             }
-            const int m = mt * 256 + int(rank) * 128 + r, c = cb * 128;
-            if (go && inside && m < M) {
-                const int64_t row = int64_t(m) * C;
-                if ((C & 7) == 0 && c + CW <= C) {
+            
+            // the tile leaves through shared memory, 32 rows x 32 columns at a time, so that the
+            // stores of a warp lie in whole rows and the accumulators are read with fixed indexes
+            const int c0 = ct * 256 + cg * CW, mrow = mt * 256 + int(rank) * 128 + q * 32;
+            float* stg = reinterpret_cast<float*>(smem + G::OFF_STG) + warp * 32 * 32;
 #pragma unroll
-                    for (int j = 0; j < CW; j += 8) epi_store8(out, row + c + j, c + j, acc + j, epi);
-                } else {
+            for (int h = 0; h < CW / 32; ++h) {
 #pragma unroll
-                    for (int j = 0; j < CW; ++j)
-                        if (c + j < C) epi_store(out, row + c + j, c + j, acc[j], epi);
-                }
+                for (int j = 0; j < 16; ++j)
+                    *reinterpret_cast<unsigned long long*>(stg + stage_word(lane, 2 * j)) = acc[h * 16 + j];
+                __syncwarp();
+                if (go) store_piece(out, stg, mrow, M, c0 + h * 32, C, epi);
+                __syncwarp();
             }
         }
     }
+    
     tc_fence_before();
-    cluster_sync();
+    cluster_sync(); 
     if (warp == G::MMA_WARP) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 512);
