@@ -12,30 +12,33 @@ w4a8_status check_fp8_dtype(w4a8_dtype dt) {
     return (dt == W4A8_F32 || dt == W4A8_BF16) ? W4A8_OK : W4A8_ERR_UNSUPPORTED;
 }
 
+template <bool BF16, bool VEC>
+void launch_fp8_quant(const void* x, int M, int L, int pitch, uint8_t* q, float* s, int64_t srow, int64_t sblk,
+                      cudaStream_t stream) {
+    const int64_t n = int64_t(M) * fp8_blocks(L);
+    if (n >= int64_t(sm_count()) * 128)
+        fp8::quant_rows_kernel<BF16, VEC, 4><<<unsigned(cdiv(n, 64)), 256, 0, stream>>>(x, M, L, pitch, q, s, srow, sblk);
+    else
+        fp8::quant_rows_kernel<BF16, VEC, 1><<<unsigned(cdiv(n, 16)), 256, 0, stream>>>(x, M, L, pitch, q, s, srow, sblk);
+}
+
 // Quantises M rows of length L into codes of the given pitch and scales of the given
 // strides, in launches of less than 2^28 blocks.
 w4a8_status run_fp8_quant(const void* x, w4a8_dtype dt, int M, int L, int pitch, uint8_t* q, float* s, int64_t srow,
                           int64_t sblk, cudaStream_t stream) {
-    const int nb = fp8_blocks(L);
-    const int chunk = int((int64_t(1) << 27) / nb);
+    const int chunk = int((int64_t(1) << 27) / fp8_blocks(L));
     const bool vec = L % 8 == 0;
     for (int m0 = 0; m0 < M; m0 += chunk) {
         const int mc = M - m0 < chunk ? M - m0 : chunk;
-        const dim3 grid(unsigned(cdiv(int64_t(mc) * nb, 16)));
         const void* xc = static_cast<const char*>(x) + int64_t(m0) * L * (dt == W4A8_BF16 ? 2 : 4);
         uint8_t* qc = q + int64_t(m0) * pitch;
         float* sc = s + m0 * srow;
-        if (dt == W4A8_BF16) {
-            if (vec)
-                fp8::quant_rows_kernel<true, true><<<grid, 256, 0, stream>>>(xc, mc, L, pitch, qc, sc, srow, sblk);
-            else
-                fp8::quant_rows_kernel<true, false><<<grid, 256, 0, stream>>>(xc, mc, L, pitch, qc, sc, srow, sblk);
-        } else {
-            if (vec)
-                fp8::quant_rows_kernel<false, true><<<grid, 256, 0, stream>>>(xc, mc, L, pitch, qc, sc, srow, sblk);
-            else
-                fp8::quant_rows_kernel<false, false><<<grid, 256, 0, stream>>>(xc, mc, L, pitch, qc, sc, srow, sblk);
-        }
+        if (dt == W4A8_BF16)
+            vec ? launch_fp8_quant<true, true>(xc, mc, L, pitch, qc, sc, srow, sblk, stream)
+                : launch_fp8_quant<true, false>(xc, mc, L, pitch, qc, sc, srow, sblk, stream);
+        else
+            vec ? launch_fp8_quant<false, true>(xc, mc, L, pitch, qc, sc, srow, sblk, stream)
+                : launch_fp8_quant<false, false>(xc, mc, L, pitch, qc, sc, srow, sblk, stream);
         const w4a8_status st = launch_status();
         if (st != W4A8_OK) return st;
     }
@@ -44,7 +47,7 @@ w4a8_status run_fp8_quant(const void* x, w4a8_dtype dt, int M, int L, int pitch,
 
 // Token tile of the few-token kernel, and the pitch of the block-major scales: whole tiles
 // are copied, so the rows are padded to the largest tile a path may take (256 for CTA pairs).
-inline int fp8_token_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+inline int fp8_token_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 inline int fp8_scale_pitch(int M) { return M <= 64 ? fp8_token_tile(M) : int(cdiv(M, 256) * 256); }
 
 // Workspace of a contraction over R columns: the quantised rows (codes of pitch
@@ -70,29 +73,49 @@ Fp8Ws fp8_ws(void* ws, int M, int R) {
 inline bool fp8_dims_ok(int M, int N, int K) { return dims_ok(M, N) && dims_ok(K, 1) && K % 16 == 0; }
 
 // CTA pairs on 256 x 256 tiles when they occupy at least half of the SMs; otherwise tiles of
-// 128 columns and at most 128 tokens, the contracted axis split over clusters.
+// 128 columns and at most 64 tokens, the contracted axis split over clusters (512 tokens at
+// 4096 x 4096, 32 pair tiles: 27.4 us against about 25 for pairs; 256 tokens: 17 against 25).
 inline bool fp8_use_pair(int M, int C) { return M > 128 && cdiv(M, 256) * cdiv(C, 256) * 4 >= sm_count(); }
 
-template <int MN, bool TRANS>
-w4a8_status launch_fp8_rows(int M, int C, int R, const CUtensorMap& tw, const Fp8Ws& w, const float* s, int swcols,
-                            void* out, const Epilogue& epi, cudaStream_t stream) {
-    using G = fp8::RowsGeo<MN>;
-    const cudaError_t ea = smem_limit_once(fp8::gemm_rows_kernel<MN, TRANS>, G::SMEM);
-    if (ea != cudaSuccess) return cuda_status(ea);
-    CUtensorMap tx;
-    if (!encode_2d(&tx, w.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(R), uint64_t(M), uint64_t(w.pitch), 128, MN,
-                   CU_TENSOR_MAP_SWIZZLE_128B))
-        return W4A8_ERR_CUDA;
-    const int64_t tiles = cdiv(C, 128) * cdiv(M, MN);
-    const int nblk = fp8_blocks(R);
-    int64_t ks = int64_t(sm_count()) * G::CTAS / tiles;
-    if (ks > 8) ks = 8;
-    if (ks > nblk) ks = nblk;
-    if (ks < 1) ks = 1;
+// Split of the contracted axis for the few-token kernel: the largest power of two (other
+// cluster sizes leave SMs of a GPC unused) whose CTAs are all resident, two per SM. Tiles of
+// 64 tokens stop at 4, since every CTA's partial sums are read by the others (64 tokens at 4096 x 4096:
+// 4 CTAs per tile 9.6 us, 8 CTAs 11.0; one token: 8 CTAs 6.9, 4 CTAs 7.5).
+struct Fp8Split {
+    int ks, kbs;  // CTAs per output tile, blocks per CTA
+};
+Fp8Split fp8_split(int M, int C, int R) {
+    const int tt = fp8_token_tile(M), nblk = fp8_blocks(R);
+    const int64_t tiles = cdiv(C, 128) * cdiv(M, tt), slots = int64_t(sm_count()) * 2;
+    int ks = tt == 64 ? 4 : fp8::kMaxSplit;
+    while (ks > 1 && (tiles * ks > slots || ks > nblk)) ks >>= 1;
     const int kbs = int(cdiv(nblk, ks));
-    ks = cdiv(nblk, kbs);  // every CTA has at least one block
+    return Fp8Split{int(cdiv(nblk, kbs)), kbs};  // every CTA has at least one block
+}
+// Whether the few-token kernel quantises the activation itself: rows that can be read eight
+// elements at a time, and at most 64 token blocks per CTA (two rounds of its 8 groups of
+// lanes), each done again by every column tile. One token at 4096 x 4096: 6.3 us against 7.0 with
+// the kernel of its own, and one launch less; 16 tokens: 8.0 against 7.5 on the device, less
+// than the launch costs the host.
+bool fp8_fused(int M, int C, int R) {
+    if (M > 16 || R % 8 != 0) return false;
+    const Fp8Split sp = fp8_split(M, C, R);
+    return sp.kbs <= fp8::RowsGeo<16, true>::XBLK && M * sp.kbs <= 64;
+}
+
+template <int MN, bool TRANS, bool FUSE, bool BF16>
+w4a8_status launch_fp8_rows(int M, int C, int R, const CUtensorMap& tw, const Fp8Ws& w, const void* x, const float* s,
+                            int swcols, void* out, const Epilogue& epi, cudaStream_t stream) {
+    using G = fp8::RowsGeo<MN, FUSE>;
+    const cudaError_t ea = smem_limit_once(fp8::gemm_rows_kernel<MN, TRANS, FUSE, BF16>, G::SMEM);
+    if (ea != cudaSuccess) return cuda_status(ea);
+    CUtensorMap tx = tw;  // not read by the fused form
+    if (!FUSE && !encode_2d(&tx, w.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(R), uint64_t(M), uint64_t(w.pitch), 128,
+                            MN, CU_TENSOR_MAP_SWIZZLE_128B))
+        return W4A8_ERR_CUDA;
+    const Fp8Split sp = fp8_split(M, C, R);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(ks), unsigned(cdiv(C, 128)), unsigned(cdiv(M, MN)));
+    cfg.gridDim = dim3(unsigned(sp.ks), unsigned(cdiv(C, 128)), unsigned(cdiv(M, MN)));
     cfg.blockDim = dim3(G::THREADS);
     cfg.dynamicSmemBytes = G::SMEM;
     cfg.stream = stream;
@@ -100,13 +123,13 @@ w4a8_status launch_fp8_rows(int M, int C, int R, const CUtensorMap& tw, const Fp
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(ks);
+    attr[1].val.clusterDim.x = unsigned(sp.ks);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cuda_status(cudaLaunchKernelEx(&cfg, fp8::gemm_rows_kernel<MN, TRANS>, M, C, R, tw, tx, (const float*)w.s,
-                                          w.spitch, s, swcols, kbs, out, epi));
+    return cuda_status(cudaLaunchKernelEx(&cfg, fp8::gemm_rows_kernel<MN, TRANS, FUSE, BF16>, M, C, R, tw, tx,
+                                          (const float*)w.s, w.spitch, x, s, swcols, sp.kbs, out, epi));
 }
 
 template <bool TRANS>
@@ -143,15 +166,18 @@ w4a8_status fp8_gemm_impl(int M, int N, int K, const void* in, w4a8_dtype dt, co
     if (!encode_2d(&tw, q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(K), uint64_t(N), uint64_t(K), 128, 128,
                    CU_TENSOR_MAP_SWIZZLE_128B))
         return W4A8_ERR_CUDA;
+    const int swcols = fp8_blocks(K);
+    const bool pair = fp8_use_pair(M, C);
+    if (!pair && fp8_fused(M, C, R))
+        return dt == W4A8_BF16 ? launch_fp8_rows<16, TRANS, true, true>(M, C, R, tw, w, in, s, swcols, out, epi, stream)
+                               : launch_fp8_rows<16, TRANS, true, false>(M, C, R, tw, w, in, s, swcols, out, epi, stream);
     const w4a8_status st = run_fp8_quant(in, dt, M, R, w.pitch, w.q, w.s, 1, w.spitch, stream);
     if (st != W4A8_OK) return st;
-    const int swcols = fp8_blocks(K);
-    if (fp8_use_pair(M, C)) return launch_fp8_pair<TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
+    if (pair) return launch_fp8_pair<TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
     switch (fp8_token_tile(M)) {
-        case 16: return launch_fp8_rows<16, TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
-        case 32: return launch_fp8_rows<32, TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
-        case 64: return launch_fp8_rows<64, TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
-        default: return launch_fp8_rows<128, TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
+        case 16: return launch_fp8_rows<16, TRANS, false, false>(M, C, R, tw, w, in, s, swcols, out, epi, stream);
+        case 32: return launch_fp8_rows<32, TRANS, false, false>(M, C, R, tw, w, in, s, swcols, out, epi, stream);
+        default: return launch_fp8_rows<64, TRANS, false, false>(M, C, R, tw, w, in, s, swcols, out, epi, stream);
     }
 }
 

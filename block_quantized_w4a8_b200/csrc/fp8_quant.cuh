@@ -76,25 +76,38 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 // Rows of length L: 16 lanes per 128-block, 8 elements each. Codes at q[m * pitch + k]
 // (pitch a multiple of 8; with a pitch beyond L the rest of the row's last 8-group is
 // written with zeros), the scale of (row m, block b) at s[m * srow + b * sblk].
-template <bool BF16, bool VEC>
+// U blocks per thread, their loads issued together (U = 4 where that still leaves every SM 128
+// blocks).
+template <bool BF16, bool VEC, int U>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const void* __restrict__ x, int M, int L, int pitch,
                                                          uint8_t* __restrict__ q, float* __restrict__ s, int64_t srow,
                                                          int64_t sblk) {
     pdl_launch_dependents();
-    const int nb = (L + kBlk - 1) / kBlk;
-    const uint32_t i = (blockIdx.x * 256u + threadIdx.x) >> 4;  // block of the matrix (M * nb < 2^28 per launch)
+    const uint32_t nb = uint32_t(L + kBlk - 1) / kBlk, n = uint32_t(M) * nb;  // n < 2^28 per launch
+    const uint32_t i0 = blockIdx.x * (16u * U) + (threadIdx.x >> 4);          // this thread's blocks: i0 + 16 u
     const int lane = threadIdx.x & 15;
-    const bool valid = i < uint32_t(M) * uint32_t(nb);
-    const int m = valid ? int(i / uint32_t(nb)) : 0, b = valid ? int(i % uint32_t(nb)) : 0;
-    const int k = b * kBlk + lane * 8;
-    float v[8];
-    load8<BF16, VEC>(x, int64_t(m) * L + k, valid ? L - k : 0, v);
-    float a = amax8(v);
+    float v[U][8];
+    int m[U], b[U];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const float sc = block_scale(a);
-    if (valid && k < L) *reinterpret_cast<uint2*>(q + int64_t(m) * pitch + k) = codes8(v, __frcp_rn(sc));
-    if (valid && lane == 0) s[m * srow + b * sblk] = sc;
+    for (int u = 0; u < U; ++u) {
+        const uint32_t i = i0 + 16u * u;
+        m[u] = int(i / nb);
+        b[u] = int(i - uint32_t(m[u]) * nb);
+        const int k = b[u] * kBlk + lane * 8;
+        load8<BF16, VEC>(x, int64_t(m[u]) * L + k, i < n ? L - k : 0, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float a = amax8(v[u]);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        const float sc = block_scale(a);
+        const int k = b[u] * kBlk + lane * 8;
+        if (i0 + 16u * u < n) {
+            if (k < L) *reinterpret_cast<uint2*>(q + int64_t(m[u]) * pitch + k) = codes8(v[u], __frcp_rn(sc));
+            if (lane == 0) s[m[u] * srow + b[u] * sblk] = sc;
+        }
+    }
 }
 
 // One CTA per 128 x 128 tile of an N x K weight (K a multiple of 16), the tile held in

@@ -53,9 +53,9 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, 
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
 __device__ __forceinline__ void tmem_load(uint32_t t, uint32_t (&r)[16]) { tmem_ld_32x32_x16(t, r); }
@@ -95,29 +95,34 @@ __device__ __forceinline__ void drain_inline(uint32_t bar, uint32_t parity, unsi
 
 constexpr int kMaxStages = 8;
 constexpr int kMaxBufs = 8;
+constexpr int kMaxSplit = 8;  // CTAs that share the contracted axis (a portable cluster)
 
 // ------------------------------------------------------------------ few tokens
-// Weights on the MMA's 128 rows, MN tokens (16 to 128) as its columns: each weight tile is
+// Weights on the MMA's 128 rows, MN tokens (16, 32 or 64) as its columns: each weight tile is
 // read once per token tile. The blocks of the contracted axis are split over a cluster of up
 // to 8 CTAs, whose partial sums are added through distributed shared memory in a fixed order.
-template <int MN_>
+// FUSE (a handful of token blocks per CTA): the CTA quantises its share of the activation
+// itself, while the first weight tiles arrive, and no other kernel runs.
+template <int MN_, bool FUSE>
 struct RowsGeo {
     static constexpr int MN = MN_;
-    static constexpr int STAGE = kTile + MN * 128;
-    static constexpr int CTAS = MN <= 64 ? 2 : 1;             // CTAs per SM
-    static constexpr int NS = MN == 16 ? 6 : MN == 32 ? 5 : MN == 64 ? 4 : 6;
-    static constexpr int NBUF = MN <= 64 ? 4 : 4;             // tensor-memory tiles
-    static constexpr int COLS = MN * NBUF < 32 ? 32 : MN * NBUF;
-    static constexpr int CW = MN <= 64 ? MN : 64;             // columns per epilogue warp
-    static constexpr int EPI_WARPS = 4 * MN / CW;
+    static constexpr int STAGE = kTile + (FUSE ? 0 : MN * 128);
+    static constexpr int NS = FUSE ? 5 : MN == 16 ? 6 : MN == 32 ? 5 : 4;
+    static constexpr int NBUF = 4;                            // tensor-memory tiles
+    static constexpr int COLS = MN * NBUF;
+    static constexpr int CW = MN;                             // columns per epilogue warp
+    static constexpr int EPI_WARPS = 4;
     static constexpr int LD = CW < 32 ? 16 : 32;
     static constexpr int COPY_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1;
     static constexpr int THREADS = (EPI_WARPS + 2) * 32;
-    static constexpr int OFF_SX = NS * STAGE;                 // token scales, one row per stage
-    static constexpr int OFF_CTRL = OFF_SX + NS * MN * 4;
+    static constexpr int XBLK = 12;                           // FUSE: blocks of the quantised activation
+    static constexpr int OFF_X = NS * STAGE;
+    static constexpr int OFF_SX = OFF_X + (FUSE ? XBLK * MN * 128 : 0);  // token scales, one row per stage (block)
+    static constexpr int OFF_CTRL = OFF_SX + (FUSE ? XBLK : NS) * MN * 4;
     static constexpr int SMEM = OFF_CTRL + 512 + 1024;
     static_assert(128 * MN * 4 <= NS * STAGE, "partial sums fit the stages");
-    static_assert(NS <= kMaxStages && NBUF <= kMaxBufs && SMEM <= (CTAS == 2 ? 115712 : 232448), "shared memory");
+    static_assert(NS <= kMaxStages && NBUF <= kMaxBufs && SMEM <= 115712, "two CTAs per SM");
+    static_assert(!FUSE || MN == 16, "the fused form is for a few tokens");
 };
 struct RowsCtrl {
     unsigned long long full[kMaxStages];   // TMA: 1 arrival + bytes
@@ -125,18 +130,22 @@ struct RowsCtrl {
     unsigned long long tfull[kMaxBufs];    // MMA commit
     unsigned long long tempty[kMaxBufs];   // one arrival per epilogue warp
     unsigned long long drain;
+    unsigned long long xready;             // FUSE: one arrival per epilogue warp
     uint32_t tmem_base;
     uint32_t abort;
 };
 static_assert(sizeof(RowsCtrl) <= 512, "control block");
 
 // Grid: x = split of the contracted axis (the cluster), y = 128-column tile, z = token tile.
-template <int MN, bool TRANS>
-__global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
+// The activation: codes through tm_x and scales sx, or (FUSE) x itself, BF16 or f32, R a
+// multiple of 8.
+template <int MN, bool TRANS, bool FUSE, bool BF16>
+__global__ void __launch_bounds__(RowsGeo<MN, FUSE>::THREADS, 2)
     gemm_rows_kernel(int M, int C, int R, const __grid_constant__ CUtensorMap tm_w,
                      const __grid_constant__ CUtensorMap tm_x, const float* __restrict__ sx, int spitch,
-                     const float* __restrict__ sw, int swcols, int kbs, void* __restrict__ out, Epilogue epi) {
-    using G = RowsGeo<MN>;
+                     const void* x, const float* __restrict__ sw, int swcols, int kbs, void* __restrict__ out,
+                     Epilogue epi) {
+    using G = RowsGeo<MN, FUSE>;
     constexpr int NS = G::NS, NBUF = G::NBUF, CW = G::CW, LD = G::LD;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -160,6 +169,7 @@ __global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
             mbar_init(bar(&ctrl->tempty[j]), G::EPI_WARPS);
         }
         mbar_init(bar(&ctrl->drain), 1);
+        mbar_init(bar(&ctrl->xready), G::EPI_WARPS);
         ctrl->abort = 0;
         mbar_init_fence();
     }
@@ -179,11 +189,12 @@ __global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
         const bool leader = elect_one();
         auto load_w = [&](int it) {
             const uint32_t fb = bar(&ctrl->full[it % NS]);
-            mbar_arrive_expect_tx(fb, uint32_t(G::STAGE + MN * 4));
+            mbar_arrive_expect_tx(fb, uint32_t(FUSE ? kTile : G::STAGE + MN * 4));
             const int r = (b0 + it) * kBlk;
             tma_load_2d<1>(smem0 + (it % NS) * G::STAGE, &tm_w, TRANS ? c0 : r, TRANS ? r : c0, fb);
         };
         auto load_x = [&](int it) {
+            if (FUSE) return;
             const uint32_t fb = bar(&ctrl->full[it % NS]);
             tma_load_2d<1>(smem0 + (it % NS) * G::STAGE + kTile, &tm_x, (b0 + it) * kBlk, m0, fb);
             bulk_g2s(smem_addr(ssx + (it % NS) * MN), sx + int64_t(b0 + it) * spitch + m0, MN * 4, fb);
@@ -192,7 +203,7 @@ __global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
         const int pre = min(NS, Bl);
         if (leader)
             for (int it = 0; it < pre; ++it) load_w(it);
-        pdl_wait_primary();
+        if (!FUSE) pdl_wait_primary();
         if (leader)
             for (int it = 0; it < pre; ++it) load_x(it);
         __syncwarp();
@@ -212,16 +223,18 @@ __global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
         const bool leader = elect_one();
         uint32_t local_abort = 0;
         constexpr uint32_t idesc = idesc_e4m3(128, MN, TRANS, false);
-        for (int it = 0; it < Bl; ++it) {
+        const bool go = !FUSE || bounded_wait_warp(bar(&ctrl->xready), 0, abort);
+        for (int it = 0; it < Bl && go; ++it) {
             const int slot = it % NS, buf = it % NBUF;
             if (!bounded_wait_warp(bar(&ctrl->full[slot]), (it / NS) & 1, abort)) break;
             if (!bounded_wait_warp(bar(&ctrl->tempty[buf]), ((it / NBUF) & 1) ^ 1, abort)) break;
             tc_fence_after();
             if (leader) {
-                const uint32_t w = smem0 + slot * G::STAGE, x = w + kTile;
+                const uint32_t w = smem0 + slot * G::STAGE;
+                const uint32_t xa = FUSE ? smem0 + G::OFF_X + it * MN * 128 : w + kTile;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f8(tmem_base + buf * MN, desc_sw128(w + k_offset<TRANS>(kk)), desc_sw128(x + k_offset<false>(kk)),
+                    mma_f8(tmem_base + buf * MN, desc_sw128(w + k_offset<TRANS>(kk)), desc_sw128(xa + k_offset<false>(kk)),
                            idesc, kk != 0);
                 tc_commit(bar(&ctrl->tfull[buf]));
             }
@@ -231,8 +244,38 @@ __global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
         __syncwarp();
         bounded_wait_warp(bar(&ctrl->drain), 0, &local_abort);
     } else {
-        const int q = warp & 3, j0 = (warp >> 2) * CW;
-        const uint32_t lane_base = tmem_base + (uint32_t(q * 32) << 16) + j0;
+        const uint32_t lane_base = tmem_base + (uint32_t(warp * 32) << 16);
+        if constexpr (FUSE) {
+            // 16 lanes per token and block, as quant_rows_kernel; codes into the operand's layout
+            // (rows of 128 bytes, 128-byte swizzle). Rows past M keep what the memory held: they
+            // only reach columns that are not stored.
+            pdl_wait_primary();
+            const int sub = lane & 15, tokens = min(MN, M - m0), n = tokens * Bl;
+            for (int w0 = warp * 2; w0 < n; w0 += 32) {  // the same trips for both half-warps
+                float v[4][8];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = w0 + (lane >> 4) + 8 * u, b = i / tokens, j = i - b * tokens, k = (b0 + b) * kBlk + sub * 8;
+                    load8<BF16, true>(x, int64_t(m0 + j) * R + k, i < n ? R - k : 0, v[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = w0 + (lane >> 4) + 8 * u, b = i / tokens, j = i - b * tokens;
+                    float a = amax8(v[u]);
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o, 16));
+                    const float sc = block_scale(a);
+                    if (i < n) {
+                        *reinterpret_cast<uint2*>(smem + G::OFF_X + b * MN * 128 + j * 128 + (((sub >> 1) ^ (j & 7)) << 4) +
+                                                  (sub & 1) * 8) = codes8(v[u], __frcp_rn(sc));
+                        if (sub == 0) ssx[b * MN + j] = sc;
+                    }
+                }
+            }
+            fence_proxy_async_smem();  // read by the tensor core
+            named_barrier(1, 128);     // the scales are read by all four warps
+            if (lane == 0) mbar_arrive(bar(&ctrl->xready));
+        }
 #pragma unroll
         for (int j = 0; j < CW; ++j) acc[j] = 0.0f;
         const float* swp = TRANS ? sw + int64_t(b0) * swcols + blockIdx.y : sw + int64_t(blockIdx.y) * swcols + b0;
@@ -243,7 +286,7 @@ __global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
             const float w = wnext;
             if (it + 1 < Bl) wnext = __ldg(swp + (it + 1) * swstep);
             if (!bounded_wait_warp(bar(&ctrl->tfull[buf]), (it / NBUF) & 1, abort)) break;
-            if (!bounded_wait_warp(bar(&ctrl->full[slot]), (it / NS) & 1, abort)) break;  // the scales' copy
+            if (!FUSE && !bounded_wait_warp(bar(&ctrl->full[slot]), (it / NS) & 1, abort)) break;  // the scales' copy
             tc_fence_after();
 #pragma unroll
             for (int h = 0; h < CW; h += LD) {
@@ -252,7 +295,7 @@ __global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
                 float s[LD];
 #pragma unroll
                 for (int j = 0; j < LD; j += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(ssx + slot * MN + j0 + h + j);
+                    const float4 v = *reinterpret_cast<const float4*>(ssx + (FUSE ? it : slot) * MN + h + j);
                     s[j] = v.x; s[j + 1] = v.y; s[j + 2] = v.z; s[j + 3] = v.w;
                 }
                 tmem_wait(p);
@@ -278,26 +321,51 @@ __global__ void __launch_bounds__(RowsGeo<MN>::THREADS, RowsGeo<MN>::CTAS)
         float* red = reinterpret_cast<float*>(smem);
         __syncthreads();
         if (warp < G::EPI_WARPS) {
-            const int j0 = (warp >> 2) * CW;
 #pragma unroll
-            for (int j = 0; j < CW; ++j) red[(j0 + j) * 128 + (warp & 3) * 32 + lane] = acc[j];
+            for (int j = 0; j < CW; ++j) red[j * 128 + warp * 32 + lane] = acc[j];
         }
         cluster_sync();
         if (!*abort) {
-            for (int i = blockIdx.x * 128 + threadIdx.x; threadIdx.x < 128 && i < tokens * 128; i += ks * 128) {
-                float v = 0.0f;
-                for (int z = 0; z < ks; ++z) v = __fadd_rn(v, ld_cluster(mapa_shared(smem0 + i * 4, z)));
-                const int c = c0 + (i & 127);
-                if (c < C) epi_store(out, int64_t(m0 + (i >> 7)) * C + c, c, v, epi);
+            // this CTA's share of the tokens, four columns per thread; the partial sums of all
+            // CTAs are requested before the first is added
+            const int per = (tokens + ks - 1) / ks, t1 = min(tokens, (int(blockIdx.x) + 1) * per);
+            const int col = (threadIdx.x & 31) * 4, c = c0 + col;
+            if (c < C) {
+#pragma unroll 2
+                for (int t = blockIdx.x * per + (threadIdx.x >> 5); t < t1; t += G::THREADS / 32) {
+                    const uint32_t at = smem0 + uint32_t(t * 128 + col) * 4;
+                    float4 v[kMaxSplit];
+#pragma unroll
+                    for (int z = 0; z < kMaxSplit; ++z)
+                        if (z < ks) v[z] = ld_cluster4(mapa_shared(at, z));
+                    float4 a = v[0];
+#pragma unroll
+                    for (int z = 1; z < kMaxSplit; ++z)
+                        if (z < ks) {
+                            a.x = __fadd_rn(a.x, v[z].x);
+                            a.y = __fadd_rn(a.y, v[z].y);
+                            a.z = __fadd_rn(a.z, v[z].z);
+                            a.w = __fadd_rn(a.w, v[z].w);
+                        }
+                    const int64_t o = int64_t(m0 + t) * C + c;
+                    if ((C & 3) == 0) {
+                        epi_store4(out, o, c, a.x, a.y, a.z, a.w, epi);
+                    } else {
+                        epi_store(out, o, c, a.x, epi);
+                        if (c + 1 < C) epi_store(out, o + 1, c + 1, a.y, epi);
+                        if (c + 2 < C) epi_store(out, o + 2, c + 2, a.z, epi);
+                        if (c + 3 < C) epi_store(out, o + 3, c + 3, a.w, epi);
+                    }
+                }
             }
         }
         cluster_sync();  // no CTA leaves while another reads its partial sums
     } else if (warp < G::EPI_WARPS && !*abort) {
-        const int j0 = (warp >> 2) * CW, c = c0 + (warp & 3) * 32 + lane;
+        const int c = c0 + warp * 32 + lane;
         if (c < C) {
 #pragma unroll
             for (int j = 0; j < CW; ++j)
-                if (j0 + j < tokens) epi_store(out, int64_t(m0 + j0 + j) * C + c, c, acc[j], epi);
+                if (j < tokens) epi_store(out, int64_t(m0 + j) * C + c, c, acc[j], epi);
         }
     }
     tc_fence_before();
