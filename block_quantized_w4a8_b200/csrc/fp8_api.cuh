@@ -12,33 +12,21 @@ w4a8_status check_fp8_dtype(w4a8_dtype dt) {
     return (dt == W4A8_F32 || dt == W4A8_BF16) ? W4A8_OK : W4A8_ERR_UNSUPPORTED;
 }
 
-template <bool BF16, bool VEC>
-void launch_fp8_quant(const void* x, int M, int L, int pitch, uint8_t* q, float* s, int64_t srow, int64_t sblk,
-                      cudaStream_t stream) {
-    const int64_t n = int64_t(M) * fp8_blocks(L);
-    if (n >= int64_t(sm_count()) * 128)
-        fp8::quant_rows_kernel<BF16, VEC, 4><<<unsigned(cdiv(n, 64)), 256, 0, stream>>>(x, M, L, pitch, q, s, srow, sblk);
-    else
-        fp8::quant_rows_kernel<BF16, VEC, 1><<<unsigned(cdiv(n, 16)), 256, 0, stream>>>(x, M, L, pitch, q, s, srow, sblk);
-}
-
 // Quantises M rows of length L into codes of the given pitch and scales of the given
 // strides, in launches of less than 2^28 blocks.
 w4a8_status run_fp8_quant(const void* x, w4a8_dtype dt, int M, int L, int pitch, uint8_t* q, float* s, int64_t srow,
                           int64_t sblk, cudaStream_t stream) {
     const int chunk = int((int64_t(1) << 27) / fp8_blocks(L));
-    const bool vec = L % 8 == 0;
+    const bool vec = L % 16 == 0;
     for (int m0 = 0; m0 < M; m0 += chunk) {
         const int mc = M - m0 < chunk ? M - m0 : chunk;
         const void* xc = static_cast<const char*>(x) + int64_t(m0) * L * (dt == W4A8_BF16 ? 2 : 4);
         uint8_t* qc = q + int64_t(m0) * pitch;
         float* sc = s + m0 * srow;
-        if (dt == W4A8_BF16)
-            vec ? launch_fp8_quant<true, true>(xc, mc, L, pitch, qc, sc, srow, sblk, stream)
-                : launch_fp8_quant<true, false>(xc, mc, L, pitch, qc, sc, srow, sblk, stream);
-        else
-            vec ? launch_fp8_quant<false, true>(xc, mc, L, pitch, qc, sc, srow, sblk, stream)
-                : launch_fp8_quant<false, false>(xc, mc, L, pitch, qc, sc, srow, sblk, stream);
+        const dim3 grid(unsigned(cdiv(int64_t(mc) * fp8_blocks(L), 32)));
+        auto* kernel = dt == W4A8_BF16 ? (vec ? fp8::quant_rows_kernel<true, true> : fp8::quant_rows_kernel<true, false>)
+                                       : (vec ? fp8::quant_rows_kernel<false, true> : fp8::quant_rows_kernel<false, false>);
+        kernel<<<grid, 256, 0, stream>>>(xc, mc, L, pitch, qc, sc, srow, sblk);
         const w4a8_status st = launch_status();
         if (st != W4A8_OK) return st;
     }

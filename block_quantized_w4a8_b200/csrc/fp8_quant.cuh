@@ -73,41 +73,32 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
     return a;
 }
 
-// Rows of length L: 16 lanes per 128-block, 8 elements each. Codes at q[m * pitch + k]
-// (pitch a multiple of 8; with a pitch beyond L the rest of the row's last 8-group is
-// written with zeros), the scale of (row m, block b) at s[m * srow + b * sblk].
-// U blocks per thread, their loads issued together (U = 4 where that still leaves every SM 128
-// blocks).
-template <bool BF16, bool VEC, int U>
+// Rows of length L: 8 lanes per 128-block, 16 elements each (half the scale arithmetic per
+// element of 16 lanes: the kernel is bound by its instructions, not by the bytes, for bf16).
+// Codes at q[m * pitch + k] (pitch a multiple of 16; with a pitch beyond L the rest of the row's
+// last 16 are written with zeros), the scale of (row m, block b) at s[m * srow + b * sblk].
+// VEC: L a multiple of 16. One block per group of lanes (two or four were no faster).
+template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const void* __restrict__ x, int M, int L, int pitch,
                                                          uint8_t* __restrict__ q, float* __restrict__ s, int64_t srow,
                                                          int64_t sblk) {
     pdl_launch_dependents();
     const uint32_t nb = uint32_t(L + kBlk - 1) / kBlk, n = uint32_t(M) * nb;  // n < 2^28 per launch
-    const uint32_t i0 = blockIdx.x * (16u * U) + (threadIdx.x >> 4);          // this thread's blocks: i0 + 16 u
-    const int lane = threadIdx.x & 15;
-    float v[U][8];
-    int m[U], b[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t i = i0 + 16u * u;
-        m[u] = int(i / nb);
-        b[u] = int(i - uint32_t(m[u]) * nb);
-        const int k = b[u] * kBlk + lane * 8;
-        load8<BF16, VEC>(x, int64_t(m[u]) * L + k, i < n ? L - k : 0, v[u]);
+    const uint32_t i = blockIdx.x * 32u + (threadIdx.x >> 3);
+    const int lane = threadIdx.x & 7;
+    const uint32_t m = i / nb, b = i - m * nb;
+    const int k = int(b) * kBlk + lane * 16, left = i < n ? L - k : 0;
+    float v[2][8];
+    load8<BF16, VEC>(x, int64_t(m) * L + k, left, v[0]);
+    load8<BF16, VEC>(x, int64_t(m) * L + k + 8, left - 8, v[1]);
+    const float sc = block_scale(warp_max8(fmaxf(amax8(v[0]), amax8(v[1]))));
+    if (i >= n) return;
+    const float inv = __frcp_rn(sc);
+    if (k < L) {
+        const uint2 lo = codes8(v[0], inv), hi = codes8(v[1], inv);
+        *reinterpret_cast<uint4*>(q + int64_t(m) * pitch + k) = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        float a = amax8(v[u]);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const float sc = block_scale(a);
-        const int k = b[u] * kBlk + lane * 8;
-        if (i0 + 16u * u < n) {
-            if (k < L) *reinterpret_cast<uint2*>(q + int64_t(m[u]) * pitch + k) = codes8(v[u], __frcp_rn(sc));
-            if (lane == 0) s[m[u] * srow + b[u] * sblk] = sc;
-        }
-    }
+    if (lane == 0) s[m * srow + b * sblk] = sc;
 }
 
 // One CTA per 128 x 128 tile of an N x K weight (K a multiple of 16), the tile held in
