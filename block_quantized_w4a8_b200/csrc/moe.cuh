@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(256, 1) route_kernel(int E, int H, int top_k, 
 // pass of its own over the expert's weights.
 struct Lists {
     float* w;        // [n] weight of a slot (folded)
-    uint16_t* ord;   // [n] slots by expert
+    uint16_t* ord;   // [n] entries by expert: slot | token << 10
     uint16_t* act;   // [groups] expert of a group, in rising order
     uint16_t* from;  // [groups] first entry
     uint8_t* cnt;    // [groups] tokens
@@ -191,6 +191,8 @@ __host__ __device__ __forceinline__ int max_groups(int E, int n, int group) { re
 __host__ __device__ __forceinline__ size_t lists_bytes(int E, int n, int group) {
     return 16 + size_t(n) * 4 + (size_t(max_groups(E, n, group)) * 5 + size_t(n) * 2 + 15) / 16 * 16;
 }
+constexpr int kSlotMask = 1023;  // slots are below kMaxTokens * kMaxTopK
+static_assert(kMaxTokens * kMaxTopK <= kSlotMask + 1 && kMaxTokens <= 64, "slot and token fit 16 bits");
 // `scratch`: at most 4 n + 4 E + E n / 32 bytes (13 KB), free once the lists are built.
 __device__ __forceinline__ Lists lists_at(uint8_t* p, uint8_t* scratch, int E, int n, int group) {
     const int m = max_groups(E, n, group);
@@ -245,7 +247,7 @@ __device__ __forceinline__ void build_lists(const Lists& l, const int* ids, cons
                 grp += kj < key && ((lead >> j) & 1u);
             }
             if (valid) {
-                l.ord[pos] = uint16_t(lane);
+                l.ord[pos] = uint16_t(lane | t << 10);
                 l.w[lane] = w;
                 if ((lead >> lane) & 1u) {
                     l.act[grp] = uint16_t(id);
@@ -265,7 +267,7 @@ __device__ __forceinline__ void build_lists(const Lists& l, const int* ids, cons
     const int chunks = (n + 31) / 32;
     for (int e = threadIdx.x; e < chunks * E; e += 256) l.hist[e] = 0;
     __syncthreads();
-    int mine[kMaxSlotsPerThread];
+    int mine[kMaxSlotsPerThread], tok[kMaxSlotsPerThread];
     int rank[kMaxSlotsPerThread];  // among the 32 slots of this warp's chunk
     float wsum[kMaxSlotsPerThread];
 #pragma unroll
@@ -273,8 +275,9 @@ __device__ __forceinline__ void build_lists(const Lists& l, const int* ids, cons
         const int i = threadIdx.x + 256 * k;
         mine[k] = i < n ? l.id[i] : -1;
         if (i - int(threadIdx.x & 31) >= n) continue;  // the whole warp
+        tok[k] = i / top_k;
         if (mine[k] >= 0) {
-            const int s0 = i / top_k * top_k, id = mine[k];
+            const int s0 = tok[k] * top_k, id = mine[k];
             wsum[k] = l.w[i];
             for (int s = s0; s < s0 + top_k; ++s)
                 if (s != i && l.id[s] == id) {
@@ -297,45 +300,38 @@ __device__ __forceinline__ void build_lists(const Lists& l, const int* ids, cons
         l.cur[e] = run;
     }
     __syncthreads();
-    if (threadIdx.x < 32) {  // first entries and groups: 8 experts per lane
+    if (threadIdx.x < 32) {  // first entries and groups, 32 experts at a time (packed: entries | groups << 16)
         const int lane = threadIdx.x;
-        int c[8], sum = 0, used = 0;
+        uint32_t base = 0u;
+#pragma unroll 1
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane, c = e < E ? l.cur[e] : 0;
+            const uint32_t one = uint32_t(c) | uint32_t((c + group - 1) / group) << 16;
+            uint32_t sum = one;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            c[i] = lane * 8 + i < E ? l.cur[lane * 8 + i] : 0;
-            sum += c[i];
-            used += (c[i] + group - 1) / group;
-        }
-        int a = sum, u = used;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int pa = __shfl_up_sync(0xffffffffu, a, o), pu = __shfl_up_sync(0xffffffffu, u, o);
-            if (lane >= o) {
-                a += pa;
-                u += pu;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t p = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += p;
             }
-        }
-        if (lane == 31) *l.nact = u;
-        a -= sum;
-        u -= used;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (lane * 8 + i < E) {
-                l.cur[lane * 8 + i] = a;
-                for (int g = 0; g < c[i]; g += group, ++u) {
-                    l.act[u] = uint16_t(lane * 8 + i);
-                    l.from[u] = uint16_t(a + g);
-                    l.cnt[u] = uint8_t(min(group, c[i] - g));
-                }
-                a += c[i];
+            const uint32_t at = base + sum - one;
+            const int a = int(at & 0xFFFFu);
+            int u = int(at >> 16);
+            if (e < E) l.cur[e] = a;
+            for (int g = 0; g < c; g += group, ++u) {
+                l.act[u] = uint16_t(e);
+                l.from[u] = uint16_t(a + g);
+                l.cnt[u] = uint8_t(min(group, c - g));
             }
+            base += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) *l.nact = int(base >> 16);
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMaxSlotsPerThread; ++k)
         if (mine[k] >= 0) {
             const int i = threadIdx.x + 256 * k;
-            l.ord[l.cur[mine[k]] + l.hist[(i >> 5) * E + mine[k]] + rank[k]] = uint16_t(i);
+            l.ord[l.cur[mine[k]] + l.hist[(i >> 5) * E + mine[k]] + rank[k]] = uint16_t(i | tok[k] << 10);
             l.w[i] = wsum[k];
         }
 }
@@ -576,9 +572,11 @@ __device__ __forceinline__ void init_ctrl(Ctrl* ctrl, const CUtensorMap* tq, con
 struct Group {
     int first, cnt;
     int b, s0, s1;  // rows of columns lane/4, 2c, 2c+1; for dp4a s0, s1 are tokens 0 and 1
-    template <typename Map>
-    __device__ __forceinline__ void set(const Lists& l, int g, Map row) {
+    // Rows by token (gate / up) or by slot (down).
+    template <bool TOKEN>
+    __device__ __forceinline__ void set(const Lists& l, int g) {
         const int lane = threadIdx.x & 31;
+        auto row = [](int entry) { return TOKEN ? entry >> 10 : entry & kSlotMask; };
         first = l.from[g];
         cnt = l.cnt[g];
         const bool dp = cnt <= kDp4aTokens;
@@ -655,7 +653,7 @@ __global__ void __launch_bounds__(256, 2)
         const int gi = item / IB, ib = item - gi * IB;
         const int r = int(l.act[gi]) * 2 * I + ib * 32 + rg * 16;
         Group gr;
-        gr.set(l, gi, [&](int slot) { return slot / top_k; });
+        gr.template set<true>(l, gi);
         const bool dp = gr.cnt <= kDp4aTokens;
         const int pitch = Bp * 32;
         const uint8_t* xb = xq + gr.b * pitch + (lane & 3) * 32;
@@ -702,7 +700,7 @@ __global__ void __launch_bounds__(256, 2)
         }
         __syncthreads();
         if (warp < gr.cnt) {
-            const int slot = l.ord[gr.first + warp];
+            const int slot = l.ord[gr.first + warp] & kSlotMask;
             float gate = 0.0f, up = 0.0f;
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
@@ -737,7 +735,7 @@ __host__ __device__ __forceinline__ size_t down_smem(int T, int E, int n) {
 }
 
 // Grid: x = split (the cluster), y = 32 rows of H, z = 32 tokens. The boxes of all used experts
-// for those rows are dealt round-robin to the warps of the cluster; each warp adds its sums,
+// for those rows are dealt in runs to the warps of the cluster; each warp adds its sums,
 // times the slots' weights, to a [token][row] array of its own, and the arrays are added in a
 // fixed order (within the CTA, then across the cluster through distributed shared memory).
 __global__ void __launch_bounds__(256, 2)
@@ -769,23 +767,26 @@ __global__ void __launch_bounds__(256, 2)
     __syncthreads();
     const int nact = *l.nact;
     Ring ring = make_ring(smem, ctrl);
-    auto step = [&](int& g, int& j, int by) {
-        j += by;
-        while (j >= nbox) {
-            j -= nbox;
+    // this warp's boxes of all groups' boxes in order: one run, so that a group's sums are
+    // flushed once per warp that meets it
+    const int64_t total = int64_t(nact) * nbox, s = blockIdx.x * kWarps + warp;
+    int left = int((s + 1) * total / slices - s * total / slices), pleft = left;
+    int pg = int(s * total / slices / nbox), pj = int(s * total / slices - int64_t(pg) * nbox);  // the next box to fetch
+    auto step = [&](int& g, int& j) {
+        if (++j == nbox) {
+            j = 0;
             ++g;
         }
     };
-    int pg = 0, pj = 0;  // the next box to fetch: group, box
-    step(pg, pj, blockIdx.x * kWarps + warp);
     auto fetch = [&]() {
-        if (pg >= nact || ring.dead) return;
+        if (pleft == 0 || ring.dead) return;
         if (lane == 0) {
             const int r = int(l.act[pg]) * H + n0;
             ring.issue(&tm_q, &tm_s, sc_tma, pj, r, r + 16);
         }
         ++ring.issued;
-        step(pg, pj, slices);
+        --pleft;
+        step(pg, pj);
     };
     int ug = pg, uj = pj;  // the box in hand
     fetch();
@@ -802,18 +803,18 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
             for (int t = 0; t < kDp4aTokens; ++t)
                 if (t < gr.cnt) {
-                    const int slot = l.ord[gr.first + t];
-                    float* p = yw + slot / top_k * kYPitch + lane;
-                    *p = fmaf(l.w[slot], acc.d[t], *p);
+                    const int entry = l.ord[gr.first + t];
+                    float* p = yw + (entry >> 10) * kYPitch + lane;
+                    *p = fmaf(l.w[entry & kSlotMask], acc.d[t], *p);
                 }
         } else {
 #pragma unroll
             for (int col = 0; col < 2; ++col) {
                 const int at = 2 * (lane & 3) + col;
                 if (at >= gr.cnt) continue;
-                const int slot = l.ord[gr.first + at];
-                const float w = l.w[slot];
-                float* p = yw + slot / top_k * kYPitch + (lane >> 2);
+                const int entry = l.ord[gr.first + at];
+                const float w = l.w[entry & kSlotMask];
+                float* p = yw + (entry >> 10) * kYPitch + (lane >> 2);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     float v0, v1;
@@ -827,11 +828,11 @@ __global__ void __launch_bounds__(256, 2)
     const uint8_t *xb = hq, *t0 = hq, *t1 = hq;
     const float *d0 = hd, *d1 = hd;
 #pragma unroll 1
-    while (ug < nact) {
+    for (; left > 0; --left) {
         if (ug != a) {
             if (a >= 0) flush();
             a = ug;
-            gr.set(l, a, [](int slot) { return slot; });
+            gr.template set<false>(l, a);
             xb = hq + int64_t(gr.b) * pitch + (lane & 3) * 32;
             t0 = hq + int64_t(gr.s0) * pitch;
             t1 = hq + int64_t(gr.s1) * pitch;
@@ -840,7 +841,7 @@ __global__ void __launch_bounds__(256, 2)
             acc.clear();
         }
         const int r = int(l.act[ug]) * H + n0, j = uj;
-        step(ug, uj, slices);
+        step(ug, uj);
         const int st = ring.used % kStages;
         const uint32_t cq = ring.codes + st * kStageBytes;
         const uint8_t* cs = ring.scales + st * kScaleBytes;
