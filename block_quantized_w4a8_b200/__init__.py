@@ -124,7 +124,7 @@ def _device(t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError("libw4a8 takes device tensors")
     dev = t.get_device()
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()  # torch.cuda.current_device() without its initialisation check
     if dev != cur:
         raise ValueError(f"libw4a8: tensors on cuda:{dev} while cuda:{cur} is the current device")
     return dev
@@ -640,8 +640,8 @@ def gemm_affine(x, q, s, b, group: int, path: int = PATH_AUTO, ws=None, stream=N
 
 def quant_act_fp8(x: torch.Tensor, stream=None):
     M, K = x.shape
-    q = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=x.device)
-    s = torch.empty(M, -(-K // 128), dtype=torch.float32, device=x.device)
+    q = x.new_empty((M, K), dtype=torch.float8_e4m3fn)
+    s = x.new_empty((M, -(-K // 128)), dtype=torch.float32)
     w4a8_quant_act_fp8(x, q, s, stream)
     return q, s
 
@@ -665,7 +665,7 @@ def fp8_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
 def gemm_fp8(x, q, s, bias=None, out_dtype=torch.float32, ws=None, stream=None):
     M, K = x.shape
     N = q.shape[0]
-    y = torch.empty(M, N, dtype=out_dtype, device=x.device)
+    y = x.new_empty((M, N), dtype=out_dtype)
     ws = fp8_workspace(M, N, K, x.device) if ws is None else ws
     w4a8_gemm_fp8(x, q, s, y, ws, bias, stream)
     return y
@@ -674,7 +674,7 @@ def gemm_fp8(x, q, s, bias=None, out_dtype=torch.float32, ws=None, stream=None):
 def gemm_fp8_backward(dy, q, s, out_dtype=torch.float32, ws=None, stream=None):
     M, N = dy.shape
     K = q.shape[1]
-    dx = torch.empty(M, K, dtype=out_dtype, device=dy.device)
+    dx = dy.new_empty((M, K), dtype=out_dtype)
     ws = fp8_workspace(M, N, K, dy.device) if ws is None else ws
     w4a8_gemm_fp8_backward(dy, q, s, dx, ws, stream)
     return dx
@@ -697,7 +697,7 @@ def moe_workspace(T: int, E: int, H: int, I: int, top_k: int, device="cuda") -> 
 
 def moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, out_dtype=torch.float32, ws=None, stream=None):
     T, H = x.shape
-    y = torch.empty(T, H, dtype=out_dtype, device=x.device)
+    y = x.new_empty((T, H), dtype=out_dtype)
     if ws is None:
         ws = moe_workspace(T, gu_qs.shape[0], H, gu_qs.shape[1] // 2, ids.shape[1], x.device)
     w4a8_moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, y, ws, stream)
@@ -708,9 +708,9 @@ def moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k: int, renorm: bool = T
                    stream=None):
     """(y, ids, weights) of the routed layer."""
     T, H = x.shape
-    ids = torch.empty(T, top_k, dtype=torch.int32, device=x.device)
-    weights = torch.empty(T, top_k, dtype=torch.float32, device=x.device)
-    y = torch.empty(T, H, dtype=out_dtype, device=x.device)
+    ids = x.new_empty((T, top_k), dtype=torch.int32)
+    weights = x.new_empty((T, top_k), dtype=torch.float32)
+    y = x.new_empty((T, H), dtype=out_dtype)
     if ws is None:
         ws = moe_workspace(T, gu_qs.shape[0], H, gu_qs.shape[1] // 2, top_k, x.device)
     w4a8_moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k, ids, weights, y, ws, renorm, stream)

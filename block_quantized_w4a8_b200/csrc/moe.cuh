@@ -602,9 +602,12 @@ __host__ __device__ __forceinline__ size_t gate_up_smem(int E, int n) {
     return 1024 + kRingBytes + kCtrlBytes + kRedBytes + lists_bytes(E, n, kGroup);
 }
 
-// Items: (group of at most 8 tokens of one expert, 32 rows of I), dealt round-robin to the
-// CTAs. Two warps share a K slice's boxes (one per 16 gate and 16 up rows), four slices; their
-// sums meet in shared memory, where a warp per token forms h, its block's scale and codes.
+// Items: (group of at most 8 tokens of one expert, 16 RG rows of I), dealt round-robin to the
+// CTAs. RG warps share a K slice's boxes (one per 16 gate and 16 up rows), 8 / RG slices; their
+// sums meet in shared memory, where a warp per token and 32 rows forms h, its block's scale
+// and codes. RG = 2 spreads few items over the GPU; RG = 4 (I a multiple of 64) halves what an
+// item costs beside its boxes.
+template <int RG>
 __global__ void __launch_bounds__(256, 2)
     gate_up_kernel(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* xq,
                    const float* xd, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_s,
@@ -616,7 +619,8 @@ __global__ void __launch_bounds__(256, 2)
     const int n = T * top_k;
     const Lists l = lists_at(smem + kRingBytes + kCtrlBytes + kRedBytes, smem, E, n, kGroup);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rg = warp & 1, ksl = warp >> 1;
+    constexpr int SLICES = kWarps / RG, ROWS = 16 * RG;
+    const int rg = warp % RG, ksl = warp / RG;
     init_ctrl(ctrl, &tm_q, &tm_s);
     pdl_wait_primary();  // ids, xq and xd are written by the preceding kernel
     pdl_launch_dependents();
@@ -624,14 +628,14 @@ __global__ void __launch_bounds__(256, 2)
     fence_proxy_async_smem();  // the lists' scratch lies in the ring, which TMA writes next
     __syncthreads();
     const int B = H / 32, Bp = padded_blocks(H), nbox = Bp / kBoxBlocks;
-    const int IB = I / 32, IBp = padded_blocks(I);
-    const int nitems = *l.nact * IB;
+    const int IB = I / 32, IBp = padded_blocks(I), IR = I / ROWS;
+    const int nitems = *l.nact * IR;
     Ring ring = make_ring(smem, ctrl);
     // the next box to fetch: item, box, first gate row
     int pi = blockIdx.x, pj = ksl, pr = 0;
     auto row_of = [&](int item) {
-        const int gi = item / IB;
-        return int(l.act[gi]) * 2 * I + (item - gi * IB) * 32 + rg * 16;
+        const int gi = item / IR;
+        return int(l.act[gi]) * 2 * I + (item - gi * IR) * ROWS + rg * 16;
     };
     const bool any = ksl < nbox;
     if (any && pi < nitems) pr = row_of(pi);
@@ -639,7 +643,7 @@ __global__ void __launch_bounds__(256, 2)
         if (!any || pi >= nitems || ring.dead) return;
         if (lane == 0) ring.issue(&tm_q, &tm_s, sc_tma, pj, pr, pr + I);
         ++ring.issued;
-        pj += 4;
+        pj += SLICES;
         if (pj >= nbox) {
             pj = ksl;
             pi += gridDim.x;
@@ -650,8 +654,8 @@ __global__ void __launch_bounds__(256, 2)
     fetch();
 
     for (int item = blockIdx.x; item < nitems; item += gridDim.x) {
-        const int gi = item / IB, ib = item - gi * IB;
-        const int r = int(l.act[gi]) * 2 * I + ib * 32 + rg * 16;
+        const int gi = item / IR, ir = item - gi * IR;
+        const int r = int(l.act[gi]) * 2 * I + ir * ROWS + rg * 16;
         Group gr;
         gr.template set<true>(l, gi);
         const bool dp = gr.cnt <= kDp4aTokens;
@@ -662,7 +666,7 @@ __global__ void __launch_bounds__(256, 2)
         Sums acc;
         acc.clear();
 #pragma unroll 1
-        for (int j = ksl; j < nbox; j += 4) {
+        for (int j = ksl; j < nbox; j += SLICES) {
             const int st = ring.used % kStages;
             const uint32_t cq = ring.codes + st * kStageBytes;
             const uint8_t* cs = ring.scales + st * kScaleBytes;
@@ -683,9 +687,9 @@ __global__ void __launch_bounds__(256, 2)
             ++ring.used;
             fetch();
         }
-        float* p = red + ksl * 64 * kRedPitch;
+        float* p = red + ksl * 2 * ROWS * kRedPitch;  // gate rows, up rows
         if (dp) {
-            float* q = p + ((lane >> 4) * 32 + rg * 16 + (lane & 15)) * kRedPitch;
+            float* q = p + ((lane >> 4) * ROWS + rg * 16 + (lane & 15)) * kRedPitch;
             q[0] = acc.d[0];
             q[1] = acc.d[1];
         } else {
@@ -693,25 +697,29 @@ __global__ void __launch_bounds__(256, 2)
             for (int m = 0; m < 4; ++m) {
                 float a, b;
                 unpack2(acc.m[m >> 1][m & 1], a, b);
-                float* q = p + ((m >> 1) * 32 + rg * 16 + (m & 1) * 8 + (lane >> 2)) * kRedPitch + 2 * (lane & 3);
+                float* q = p + ((m >> 1) * ROWS + rg * 16 + (m & 1) * 8 + (lane >> 2)) * kRedPitch + 2 * (lane & 3);
                 q[0] = a;
                 q[1] = b;
             }
         }
         __syncthreads();
-        if (warp < gr.cnt) {
-            const int slot = l.ord[gr.first + warp] & kSlotMask;
+        for (int tb = warp; tb < gr.cnt * (RG / 2); tb += kWarps) {  // token, 32 rows of the item
+            const int t = RG == 2 ? tb : tb >> 1, half = RG == 2 ? 0 : tb & 1;
+            const int slot = l.ord[gr.first + t] & kSlotMask, ib = ir * (RG / 2) + half;
             float gate = 0.0f, up = 0.0f;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                gate = __fadd_rn(gate, red[(s * 64 + lane) * kRedPitch + warp]);
-                up = __fadd_rn(up, red[(s * 64 + 32 + lane) * kRedPitch + warp]);
+            for (int s = 0; s < SLICES; ++s) {
+                const float* q = red + (s * 2 * ROWS + half * 32 + lane) * kRedPitch + t;
+                gate = __fadd_rn(gate, q[0]);
+                up = __fadd_rn(up, q[ROWS * kRedPitch]);
             }
             const float hv = __fmul_rn(__fdiv_rn(gate, 1.0f + expf(-gate)), up);
             float amax = fabsf(hv);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float d = __fdiv_rn(amax, 127.0f);
+            // the maximum passes over a NaN, whose code is 0: the scale carries it on
+            const bool nan = __any_sync(0xffffffffu, hv != hv);
+            const float d = nan ? __int_as_float(0x7FC00000) : __fdiv_rn(amax, 127.0f);
             const float id = d != 0.0f ? __frcp_rn(d) : 0.0f;
             const int code = max(-127, min(127, int(roundf(__fmul_rn(hv, id)))));
             uint32_t w = (uint32_t(code) & 0xFFu) << (8 * (lane & 3));

@@ -100,15 +100,19 @@ w4a8_status run_experts(int T, int E, int H, int I, int top_k, const int* ids, c
         return W4A8_ERR_CUDA;
     // limits for the largest lists, so that one setting serves every call
     const int n = T * top_k, td = T < moe::kDownTokens ? T : moe::kDownTokens;
-    cudaError_t e = smem_limit_once(moe::gate_up_kernel,
+    const int64_t items = int64_t(moe::max_groups(E, n, moe::kGroup)) * (I / 32);
+    const int64_t slots = int64_t(sm_count()) * 2;
+    // 64 rows per item where that still leaves every CTA two of them and the experts have a few
+    // tokens each, so that what an item costs beside its boxes counts (64 tokens, top 8 of 64:
+    // 112 -> 108 us; 4 tokens, top 2 of 8, where rounds of items count more: 117 -> 123)
+    auto* gate_up = I % 64 == 0 && items >= 4 * slots && n >= 2 * E ? moe::gate_up_kernel<4> : moe::gate_up_kernel<2>;
+    cudaError_t e = smem_limit_once(gate_up,
                                     int(moe::gate_up_smem(moe::kMaxExperts, moe::kMaxTokens * moe::kMaxTopK)));
     if (e == cudaSuccess)
         e = smem_limit_once(moe::down_kernel, int(moe::down_smem(moe::kDownTokens, moe::kMaxExperts,
                                                                  moe::kDownTokens * moe::kMaxTopK)));
     if (e != cudaSuccess) return cuda_status(e);
-    const int64_t items = int64_t(moe::max_groups(E, n, moe::kGroup)) * (I / 32);
-    const int64_t slots = int64_t(sm_count()) * 2;
-    e = launch_pdl(moe::gate_up_kernel, dim3(unsigned(items < slots ? items : slots)), dim3(256),
+    e = launch_pdl(gate_up, dim3(unsigned(items < slots ? items : slots)), dim3(256),
                    moe::gate_up_smem(E, n), stream, T, E, H, I, top_k, ids, weights, (const uint8_t*)w.xq,
                    (const float*)w.xd, gtq, gts, gsc, gd, w.hq, w.hd);
     if (e != cudaSuccess) return cuda_status(e);

@@ -334,8 +334,14 @@ w4a8_status w4a8_pack_fp8(const void* w, w4a8_dtype dtype, int N, int K, uint8_t
  *                           dy (M x N, f32 or bf16) quantised in the call with one scale
  *                           per row and 128 columns of N; dx M x K of dx_dtype. The weights
  *                           are frozen codes and get no gradient.
- * The products of two codes are exact; they are summed in f32. Every output is within
- * 1e-5 * sum |terms| of the exact sum over the codes (plus the rounding to bf16).
+ * The products of two codes are exact; they are summed in f32 (tensor-core sums within a
+ * block, then one rounding per block and per CTA that shares the axis). Every output is
+ * within 1e-5 * sum |terms| of the exact sum over the codes for contracted axes up to 16384,
+ * and within (length / 128 + 40) * 2^-24 * sum |terms| beyond (plus the rounding to bf16). The
+ * result does not depend on scheduling.
+ * Few rows of x run tiles of 128 columns by 16 to 64 rows, the contracted axis split over a
+ * cluster; a handful (M <= 16 with few blocks per CTA) are quantised inside that kernel, and
+ * the workspace is then only checked; from about 37 tiles of 256 x 256 on, CTA pairs.
  * ws : w4a8_fp8_workspace_bytes(M, N, K) bytes (serves both calls; query it with the device
  *      current), 16-byte aligned; contents ignored on entry, garbage afterwards. Calls that
  *      share a workspace must be ordered on one stream. Returns 0 for invalid sizes.
@@ -360,7 +366,8 @@ w4a8_status w4a8_gemm_fp8_backward(int M, int N, int K, const void* dy, w4a8_dty
  *  w4a8_moe_q4_0       : y[t] = sum_s weights[t][s] * down(e), e = ids[t][s], with
  *                          g = xq . Wg[e]^T, u = xq . Wu[e]^T   (as w4a8_gemm, xq = Q8_0(x[t]))
  *                          h = g / (1 + exp(-g)) * u            (f32)
- *                          down(e) = hq . Wd[e]^T               (hq = Q8_0(h))
+ *                          down(e) = hq . Wd[e]^T               (hq = Q8_0(h); a NaN in h makes
+ *                                                                the token's row NaN)
  *                        A slot whose id is negative or not below E is empty and adds
  *                        nothing (a token with only empty slots gets a row of zeros); an
  *                        expert named by two slots of a token counts with the sum of their weights.
@@ -372,6 +379,10 @@ w4a8_status w4a8_gemm_fp8_backward(int M, int N, int K, const void* dy, w4a8_dty
  * ws          : w4a8_moe_workspace_bytes bytes, 16-byte aligned; contents ignored on entry,
  *               garbage afterwards. Calls that share one must be ordered on one stream.
  *               Returns 0 for sizes the calls refuse.
+ * Every dot is within 1e-5 * sum |block terms| of the exact one, as w4a8_gemm; a value of h so
+ * close to a rounding border that this error carries it across changes by one step of its
+ * block. A call's result does not depend on scheduling; the order of a token's sum over
+ * experts may depend on which other experts the batch uses.
  * Limits: T <= W4A8_MOE_MAX_TOKENS (the routed calls), E <= W4A8_MOE_MAX_EXPERTS, top_k <=
  * min(E, W4A8_MOE_MAX_TOPK), I <= W4A8_MAX_DIM / 2; H and I multiples of 32.
  * Errors: INVALID_ARG (null, sizes), UNSUPPORTED (a limit, a dtype), MISALIGNED, WORKSPACE, CUDA.

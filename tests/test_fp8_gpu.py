@@ -143,6 +143,26 @@ def test_zero_rows_give_zero(M):
     assert torch.equal(y[M // 2], torch.zeros_like(y[M // 2]))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 130, 16384), (20, 130, 16384), (300, 130, 16384), (2600, 1030, 16384)])
+def test_long_sums_of_one_sign(M, N, K):
+    """All terms positive, so |y| = sum |terms|: the worst case for a long chain of f32 sums, held
+    to 1e-5 at the longest axis the header promises it for (128 blocks)."""
+    g = torch.Generator().manual_seed(K)
+    q, s = w4a8.pack_fp8(torch.rand(N, K, generator=g).cuda())
+    x = torch.rand(M, K, generator=g).cuda()
+    y = w4a8.gemm_fp8(x, q, s).double()
+    qx, sx = w4a8.quant_act_fp8(x)
+    w = q.double() * s.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)
+    want = (qx.double() * sx.double().repeat_interleave(128, 1)) @ w.T
+    assert float(((y - want).abs() / want).max()) <= TOL
+    if M > 16:  # the gradient contracts M x N: the same weights turned round
+        q2, s2 = w4a8.pack_fp8(torch.rand(K, 144, generator=g).cuda())
+        dx = w4a8.gemm_fp8_backward(x, q2, s2).double()
+        w2 = q2.double() * s2.double().repeat_interleave(128, 0).repeat_interleave(128, 1)[:, :144]
+        want = (qx.double() * sx.double().repeat_interleave(128, 1)) @ w2
+        assert float(((dx - want).abs() / want).max()) <= TOL
+
+
 # ------------------------------------------------------------------ memory, streams, graphs
 @pytest.mark.parametrize("M,N,K", [(1, 1000, 1040), (16, 129, 144), (70, 333, 400), (201, 1531, 1936),
                                    (1100, 2090, 2064)])

@@ -63,7 +63,8 @@ def verify(x, gu, dn, ids, weights, out, rel, what=""):
 # tiles, more tokens per expert than one tile of 8, all 64 tokens on one expert
 SHAPES = [(1, 1, 32, 32, 1), (1, 8, 512, 96, 2), (2, 3, 96, 32, 2), (3, 5, 160, 224, 3), (5, 4, 256, 256, 1),
           (13, 11, 736, 352, 3), (16, 2, 512, 512, 2), (40, 3, 288, 128, 2), (64, 1, 256, 64, 1), (64, 16, 512, 256, 8),
-          (1, 64, 2048, 1024, 8), (9, 2, 4096, 288, 1), (64, 9, 512, 1024, 5), (33, 4, 96, 2048, 4), (64, 256, 128, 64, 16)]
+          (1, 64, 2048, 1024, 8), (9, 2, 4096, 288, 1), (64, 9, 512, 1024, 5), (33, 4, 96, 2048, 4), (64, 256, 128, 64, 16),
+          (20, 8, 160, 4160, 6)]
 
 
 @pytest.mark.parametrize("T,E,H,I,k", SHAPES)
@@ -101,6 +102,29 @@ def test_empty_slots_repeated_experts_and_empty_tokens():
     assert torch.equal(y[1], torch.zeros_like(y[1]))
     ids[:] = -1
     assert torch.equal(run(x, gu, dn, ids, weights), torch.zeros(T, H, device="cuda"))
+
+
+@pytest.mark.parametrize("T,E,k", [(20, 5, 3), (64, 16, 16), (64, 40, 8)])
+def test_random_slots(T, E, k):
+    """Slots drawn with repeats and empty ones among them (more than 32 slots)."""
+    H, I = 96, 64
+    x, gu, dn, _, _ = make(T, E, H, I, 1, 4)
+    g = torch.Generator().manual_seed(T + k)
+    ids = torch.randint(-1, E + 1, (T, k), generator=g).int()
+    weights = torch.rand(T, k, generator=g)
+    verify(x, gu, dn, ids, weights, torch.float32, TOL)
+
+
+@pytest.mark.parametrize("T", [1, 2, 12])
+def test_nan_in_h_reaches_its_token_and_no_other(T):
+    """An infinite input block gives NaN gates (inf - inf); the tokens beside it do not change."""
+    E, H, I, k = 2, 128, 96, 2
+    x, gu, dn, ids, weights = make(T, E, H, I, k, 6)
+    y = run(x, gu, dn, ids, weights)
+    x[0, 40] = float("inf")
+    z = run(x, gu, dn, ids, weights)
+    assert not torch.isfinite(z[0]).any()
+    assert torch.equal(z[1:], y[1:])
 
 
 def test_a_token_does_not_depend_on_the_others():
