@@ -130,12 +130,20 @@ w4a8_status launch_fp8_pair(int M, int C, int R, const CUtensorMap& tw, const Fp
     if (!encode_2d(&tx, w.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(R), uint64_t(M), uint64_t(w.pitch), 128, 128,
                    CU_TENSOR_MAP_SWIZZLE_128B))
         return W4A8_ERR_CUDA;
+    // the output, in pieces of 32 rows x 128 bytes, when its rows are whole 16-byte units
+    const int esize = epi.out_bf16 ? 2 : 4;
+    const int tma_out = C % (16 / esize) == 0;
+    CUtensorMap to = tx;
+    if (tma_out && !encode_2d(&to, out, epi.out_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                              esize, uint64_t(C), uint64_t(M), uint64_t(C) * esize, uint32_t(128 / esize), 32,
+                              CU_TENSOR_MAP_SWIZZLE_128B))
+        return W4A8_ERR_CUDA;
     const int tm = int(cdiv(M, 256)), tc = int(cdiv(C, 256));
     const int64_t tiles = int64_t(tm) * tc;
     const int pairs = int(tiles < sm_count() / 2 ? tiles : sm_count() / 2);
     return cuda_status(launch_pdl(fp8::gemm_pair_fp8_kernel<TRANS>, dim3(unsigned(2 * pairs)), dim3(G::THREADS),
-                                  size_t(G::SMEM), stream, M, C, R, tw, tx, (const float*)w.s, w.spitch, s, swcols, tm,
-                                  tc, out, epi));
+                                  size_t(G::SMEM), stream, M, C, R, tw, tx, to, tma_out, (const float*)w.s, w.spitch, s,
+                                  swcols, tm, tc, out, epi));
 }
 
 // out (M x C) = in (M x R) . w, w = W^T (TRANS = false) or W (the input gradient).

@@ -473,6 +473,39 @@ __device__ __forceinline__ void store_piece(void* out, const float* stg, int m0,
     }
 }
 
+// A lane's row of a staged piece of 128 bytes, which a TMA store takes to the output: 16-byte
+// chunk c of row r at (c ^ (r & 7)) (the 128-byte swizzle). `acc` holds the row's sums in pairs
+// from column c0 on: 64 bf16 (BF16) or 32 f32 columns.
+template <bool BF16>
+__device__ __forceinline__ void stage_row(uint32_t row, int lane, const unsigned long long* acc, int c0, int C,
+                                          const Epilogue& epi) {
+    constexpr int PER = BF16 ? 8 : 4;  // columns per chunk
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+        float v[PER];
+#pragma unroll
+        for (int j = 0; j < PER / 2; ++j) unpack2(acc[ch * PER / 2 + j], v[2 * j], v[2 * j + 1]);
+        if (epi.bias) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) v[j] = epi_value(epi, min(c0 + ch * PER + j, C - 1), v[j]);
+        }
+        uint32_t w[4];
+        if constexpr (BF16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(v[j]);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + uint32_t((ch ^ (lane & 7)) << 4)), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
+    }
+}
+
 // Loads that stay where they are written (a plain __ldg may be moved down to its use).
 __device__ __forceinline__ float load_ahead(const float* p) {
     float v;
@@ -483,10 +516,9 @@ __device__ __forceinline__ float load_ahead(const float* p) {
 template <bool TRANS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
     gemm_pair_fp8_kernel(int M, int C, int R, const __grid_constant__ CUtensorMap tm_w,
-                         const __grid_constant__ CUtensorMap tm_x, const float* sx, int spitch,
-                         const float* __restrict__ sw, int swcols, int tiles_m, int tiles_c, void* __restrict__ out,
-                         Epilogue epi) {
-    
+                         const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_out, int tma_out,
+                         const float* sx, int spitch, const float* __restrict__ sw, int swcols, int tiles_m, int tiles_c,
+                         void* __restrict__ out, Epilogue epi) {
     using G = PairGeo;
     constexpr int NS = G::NS, NBUF = G::NBUF, CW = G::CW, LD = G::LD;
     extern __shared__ uint8_t smem_raw[];
@@ -524,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
     const uint32_t tmem_base = ctrl->tmem_base;
     pdl_launch_dependents();
     const uint32_t smem0 = smem_addr(smem);
-     pdl_wait_primary();  // the token operand and its scales are written by the preceding kernel
+    pdl_wait_primary();  // the token operand and its scales are written by the preceding kernel
 
     if (warp >= G::COPY_WARP) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == G::COPY_WARP) {
@@ -623,7 +655,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
                     go = false;
                     break;
                 }
-                  
                 tc_fence_after();
 #pragma unroll
                 for (int h = 0; h < CW / LD; ++h) {
@@ -646,25 +677,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo::THREADS, 1)
                                                    f2, acc[h * LD / 2 + j]);
                 }
             }
-            
-            // the tile leaves through shared memory, 32 rows x 32 columns at a time, so that the
-            // stores of a warp lie in whole rows and the accumulators are read with fixed indexes
+            // The tile leaves through shared memory, in pieces of 32 rows x 128 bytes that TMA stores
+            // take to the output while the next tile runs (rows of a multiple of 16 bytes), or 32 rows
+            // x 32 columns at a time, so that the stores of a warp lie in whole rows. Either way the
+            // accumulators are read with fixed indexes.
             const int c0 = ct * 256 + cg * CW, mrow = mt * 256 + int(rank) * 128 + q * 32;
             float* stg = reinterpret_cast<float*>(smem + G::OFF_STG) + warp * 32 * 32;
+            if (tma_out) {
+                const uint32_t stg0 = smem_addr(stg), row = stg0 + uint32_t(lane) * 128u;
+                auto send = [&](int c) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && go && c < C && mrow < M) {
+                        if (epi.out_bf16)
+                            tma_store_2d<2>(&tm_out, c, mrow, stg0);
+                        else
+                            tma_store_2d<4>(&tm_out, c, mrow, stg0);
+                        bulk_commit();
+                    }
+                    __syncwarp();
+                };
+                auto staged = [&]() {  // the previous piece has left
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+                };
+                if (epi.out_bf16) {
 #pragma unroll
-            for (int h = 0; h < CW / 32; ++h) {
+                    for (int h = 0; h < CW / 64; ++h) {
+                        staged();
+                        stage_row<true>(row, lane, acc + h * 32, c0 + h * 64, C, epi);
+                        send(c0 + h * 64);
+                    }
+                } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    *reinterpret_cast<unsigned long long*>(stg + stage_word(lane, 2 * j)) = acc[h * 16 + j];
-                __syncwarp();
-                if (go) store_piece(out, stg, mrow, M, c0 + h * 32, C, epi);
-                __syncwarp();
+                    for (int h = 0; h < CW / 32; ++h) {
+                        staged();
+                        stage_row<false>(row, lane, acc + h * 16, c0 + h * 32, C, epi);
+                        send(c0 + h * 32);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < CW / 32; ++h) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        *reinterpret_cast<unsigned long long*>(stg + stage_word(lane, 2 * j)) = acc[h * 16 + j];
+                    __syncwarp();
+                    if (go) store_piece(out, stg, mrow, M, c0 + h * 32, C, epi);
+                    __syncwarp();
+                }
             }
         }
+        if (lane == 0) bulk_wait();
+        __syncwarp();
     }
-    
+
     tc_fence_before();
-    cluster_sync(); 
+    cluster_sync();
     if (warp == G::MMA_WARP) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 512);
