@@ -60,10 +60,12 @@ Fp8Ws fp8_ws(void* ws, int M, int R) {
 
 inline bool fp8_dims_ok(int M, int N, int K) { return dims_ok(M, N) && dims_ok(K, 1) && K % 16 == 0; }
 
-// CTA pairs on 256 x 256 tiles when they occupy at least half of the SMs; otherwise tiles of
-// 128 columns and at most 64 tokens, the contracted axis split over clusters (512 tokens at
-// 4096 x 4096, 32 pair tiles: 27.4 us against about 25 for pairs; 256 tokens: 17 against 25).
-inline bool fp8_use_pair(int M, int C) { return M > 128 && cdiv(M, 256) * cdiv(C, 256) * 4 >= sm_count(); }
+// CTA pairs on 256 x 256 tiles once the few-token kernel's tiles (64 tokens x 128 columns) are more
+// than the SMs. Measured with K = 4096, pairs against the few-token kernel: 128 x 14336 (224 tiles)
+// 26.1 against 28.6 us, 192 x 14336 (336) 26.5 / 51.1, 256 x 6144 (192) 23.5 / 27.9, 320 x 4096
+// (160) 23.6 / 27.0; 256 x 4096 (128) 22.8 / 17.5, 1024 x 1024 (128) 23.1 / 18.1, 64 x 14336 (112)
+// 24.8 / 19.2; K = 1024: 300 x 4096 (160) 10.9 / 12.6; K = 8192: 512 x 2048 (128) 38.4 / 27.9.
+inline bool fp8_use_pair(int M, int C) { return M > 64 && cdiv(M, 64) * cdiv(C, 128) > sm_count(); }
 
 // Split of the contracted axis for the few-token kernel: the largest power of two (other
 // cluster sizes leave SMs of a GPC unused) whose CTAs are all resident, two per SM. Tiles of

@@ -93,6 +93,22 @@ def test_backward(M, N, K, dtype):
     assert w4a8.w4a8_last_device_error() == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(70, 18969, 144), (100, 19008, 272), (65, 19012, 128), (300, 9000, 400)])
+@pytest.mark.parametrize("bias_dtype", [None, torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_wide_outputs_with_a_bias(M, N, K, bias_dtype, dtype):
+    """Wide outputs of few rows: rows of 16-byte units or not, ends inside a tile, each bias."""
+    q, s, wq, ws = weights(N, K, N + K)
+    x = rand((M, K), M, dtype)
+    bias = None
+    if bias_dtype is not None:
+        bias = torch.randn(N, generator=torch.Generator().manual_seed(1)).to(bias_dtype)
+    y = w4a8.gemm_fp8(x.cuda(), q, s, bias=None if bias is None else bias.cuda(), out_dtype=dtype)
+    yref, T = ref.gemm(x.float().numpy(), wq, ws, None if bias is None else bias.float().numpy().astype(np.float64))
+    check(y, yref, T, f"{M}x{N}x{K}")
+    assert w4a8.w4a8_last_device_error() == 0
+
+
 def test_backward_agrees_with_differences_of_the_forward():
     """With x and dy on the e4m3 grid (scale 1 in every block, so neither call rounds its
     input), <dy, y(x + e) - y(x - e)> = <dx, 2e> up to the f32 sums of both calls."""
