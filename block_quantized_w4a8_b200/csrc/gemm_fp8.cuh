@@ -102,7 +102,10 @@ constexpr int kMaxSplit = 8;  // CTAs that share the contracted axis (a portable
 // read once per token tile. The blocks of the contracted axis are split over a cluster of up
 // to 8 CTAs, whose partial sums are added through distributed shared memory in a fixed order.
 // FUSE (a handful of token blocks per CTA): the CTA quantises its share of the activation
-// itself, while the first weight tiles arrive, and no other kernel runs.
+// itself, while the first weight tiles arrive, and no other kernel runs. The weights' bytes are the
+// bound: 16 x 14336 x 4096 takes 16.2 us with the quantisation (58.7 MB at 3.6 TB/s; 224 CTAs leave
+// half of the SMs with one), one token at 4096 x 4096 6.4 us, mostly the latency of a launch, the first
+// tiles and the join. mma.sync would need the codes widened in registers; tcgen05 reads them as they lie.
 template <int MN_, bool FUSE>
 struct RowsGeo {
     static constexpr int MN = MN_;
@@ -382,7 +385,12 @@ __global__ void __launch_bounds__(RowsGeo<MN, FUSE>::THREADS, 2)
 // tiles of 256 columns alternate, so the MMAs of the next block run while the epilogue adds
 // the last one; the output of a tile is stored while the next tile's first blocks run. A stage
 // is handed back by its MMAs' commit, not by the epilogue, which takes the token scales from
-// global memory a block ahead.
+// global memory a block ahead. 4096 x 14336 x 4096: 289 us with the quantisation (1.66 PFLOP/s); bound by
+// the chain MMA commit, tensor-memory read, release over two tiles (about 0.65 us per block of
+// 0.28 us of MMA), of which no part alone is most: without three quarters of the MMAs 20 % less time, without the
+// multiply-adds 6 %. 256-column MMAs, since each reads the token operand from shared memory: two of
+// 128 columns with hand-offs of their own were 7 % slower, and polling instead of suspending
+// waits 3 %.
 struct PairGeo {
     static constexpr int STAGE = 2 * kTile;  // token tile, weight half
     static constexpr int NS = 6;

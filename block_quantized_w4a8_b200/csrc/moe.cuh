@@ -11,7 +11,7 @@
 // The weights of the chosen experts are read once and are nearly all the traffic, so both
 // expert kernels are built around their stream: every warp runs a ring of its own, two TMA boxes
 // (16 rows x 8 blocks each) per stage, with no barrier between warps until their rows are
-// summed. The integer dots are exact. Groups of one or two tokens use dp4a, a row per lane;
+// summed. The integer dots are exact. Groups of one token use dp4a, a row per lane;
 // larger ones mma.sync.m16n8k32 on int8, one per 16 rows and quant block: the instruction's K
 // is the block, its A fragment is the packed codes as they lie in memory (one ldmatrix word
 // holds the low and high nibbles of both K halves), and 8 tokens cost what one costs. tcgen05
@@ -77,7 +77,8 @@ constexpr int kRouteCtas = 8;  // CTAs per token (the cluster)
 
 // Grid: kRouteCtas CTAs (a cluster) per token. Every CTA quantises its share of the token's
 // blocks (xq != nullptr) and, with ROUTE, computes the logits of its experts, a warp each;
-// they meet in the first CTA's shared memory, where one warp takes the top_k.
+// they meet in the first CTA's shared memory, where one warp takes the top_k. Bound by latency:
+// 64 tokens x 64 experts, H = 2048: 11.6 us alone; the experts' first weights load meanwhile.
 template <bool ROUTE, bool XB, bool WB>
 __global__ void __launch_bounds__(256, 1) route_kernel(int E, int H, int top_k, int renorm, const void* __restrict__ x,
                                                     const void* __restrict__ wr, int* __restrict__ ids,
@@ -345,7 +346,6 @@ constexpr int kTileBytes = 2048;   // 16 rows x 8 blocks of codes, 128-byte swiz
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kScaleBytes = 512;   // 2 x 16 rows x 8 fp16
 constexpr int kRingBytes = kWarps * kStages * (kStageBytes + kScaleBytes);
-constexpr int kDp4aTokens = 2;     // largest group on dp4a (see row_dp4a)
 
 // One warp's ring: two 16-row tiles of 8 blocks per stage.
 struct Ring {
@@ -487,32 +487,26 @@ __device__ __forceinline__ void stage_mma(unsigned long long (&acc)[2][2], uint3
     }
 }
 
-// The same stage for CNT tokens (1 or 2), a row per lane (row lane & 15 of tile lane >> 4), the
-// tokens' codes broadcast: 8 x (12 + 13 CNT) instructions and no idle columns, against about
-// 300 for the MMA form.
-template <bool L2, int CNT>
-__device__ __forceinline__ void stage_dp4a(float (&acc)[kDp4aTokens], uint32_t codes, const uint8_t* scales,
-                                           const uint8_t* const (&xb)[kDp4aTokens], const float* const (&db)[kDp4aTokens]) {
+// The same stage for a group of one token, a row per lane (row lane & 15 of tile lane >> 4), the
+// token's codes broadcast: about 200 instructions against 300 for the MMA form. One token on 64
+// experts of 2048 x 1024, top 8: 16.2 us against 17.6 with the MMA form alone; groups of two on
+// dp4a as well were slower (4 tokens, top 2 of 8, 4096 x 14336: 125.2 against 122.3 us).
+template <bool L2>
+__device__ __forceinline__ void stage_dp4a(float& acc, uint32_t codes, const uint8_t* scales, const uint8_t* xb,
+                                           const float* db) {
     const int lane = threadIdx.x & 31, row = lane & 15;
     const uint32_t base = codes + uint32_t(lane >> 4) * kTileBytes + uint32_t(row * 128);
     const uint4 sc = *reinterpret_cast<const uint4*>(scales + lane * 16);
     const uint32_t sw[4] = {sc.x, sc.y, sc.z, sc.w};
-    constexpr int AHEAD = CNT == 1 ? 4 : 2;  // blocks whose activations are fetched together
 #pragma unroll
-    for (int b0 = 0; b0 < 8; b0 += AHEAD) {
-        uint4 x[CNT][2 * AHEAD];
-        float4 dx[CNT];
+    for (int b0 = 0; b0 < 8; b0 += 4) {  // the activations of four blocks are fetched together
+        uint4 x[8];
 #pragma unroll
-        for (int t = 0; t < CNT; ++t) {
+        for (int i = 0; i < 8; ++i)  // word i % 4 of two blocks
+            x[i] = load_codes<L2>(xb + (b0 >> 2) * 128 + (i & 3) * 32 + (i >> 2) * 16);
+        const float4 dx = load_scales<L2>(db + b0);
 #pragma unroll
-            for (int i = 0; i < 2 * AHEAD; ++i) {  // word i % 4 of two blocks
-                const int b = b0 + i / 4 * 2;
-                x[t][i] = load_codes<L2>(xb[t] + (b >> 2) * 128 + (i & 3) * 32 + (b & 3) * 8);
-            }
-            dx[t] = load_scales<L2>(db[t] + (b0 & 4));
-        }
-#pragma unroll
-        for (int k0 = 0; k0 < AHEAD; k0 += 2) {
+        for (int k0 = 0; k0 < 4; k0 += 2) {
             const int b = b0 + k0;
             uint32_t w[2][4];
 #pragma unroll
@@ -521,20 +515,17 @@ __device__ __forceinline__ void stage_dp4a(float (&acc)[kDp4aTokens], uint32_t c
                              : "=r"(w[k][0]), "=r"(w[k][1]), "=r"(w[k][2]), "=r"(w[k][3])
                              : "r"(base + uint32_t(((b + k) ^ (row & 7)) << 4)));
             const float2 dw = halves(sw[b >> 1]);
+            int s0 = 0, s1 = 0;
 #pragma unroll
-            for (int t = 0; t < CNT; ++t) {
-                int s0 = 0, s1 = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {  // words i of blocks b and b + 1: both K halves
-                    const uint4 v = x[t][2 * k0 + i];
-                    s0 = __dp4a(int(low_codes(w[0][i])), int(v.x), s0);
-                    s1 = __dp4a(int(low_codes(w[1][i])), int(v.z), s1);
-                    s0 = __dp4a(int(high_codes(w[0][i])), int(v.y), s0);
-                    s1 = __dp4a(int(high_codes(w[1][i])), int(v.w), s1);
-                }
-                acc[t] = fmaf(float(s0), __fmul_rn(dw.x, (b & 2) ? dx[t].z : dx[t].x), acc[t]);
-                acc[t] = fmaf(float(s1), __fmul_rn(dw.y, (b & 2) ? dx[t].w : dx[t].y), acc[t]);
+            for (int i = 0; i < 4; ++i) {  // words i of blocks b and b + 1: both K halves
+                const uint4 v = x[2 * k0 + i];
+                s0 = __dp4a(int(low_codes(w[0][i])), int(v.x), s0);
+                s1 = __dp4a(int(low_codes(w[1][i])), int(v.z), s1);
+                s0 = __dp4a(int(high_codes(w[0][i])), int(v.y), s0);
+                s1 = __dp4a(int(high_codes(w[1][i])), int(v.w), s1);
             }
+            acc = fmaf(float(s0), __fmul_rn(dw.x, k0 ? dx.z : dx.x), acc);
+            acc = fmaf(float(s1), __fmul_rn(dw.y, k0 ? dx.w : dx.y), acc);
         }
     }
 }
@@ -571,7 +562,7 @@ __device__ __forceinline__ void init_ctrl(Ctrl* ctrl, const CUtensorMap* tq, con
 // (a column never reaches another).
 struct Group {
     int first, cnt;
-    int b, s0, s1;  // rows of columns lane/4, 2c, 2c+1; for dp4a s0, s1 are tokens 0 and 1
+    int b, s0, s1;  // rows of columns lane/4, 2c, 2c+1
     // Rows by token (gate / up) or by slot (down).
     template <bool TOKEN>
     __device__ __forceinline__ void set(const Lists& l, int g) {
@@ -579,19 +570,18 @@ struct Group {
         auto row = [](int entry) { return TOKEN ? entry >> 10 : entry & kSlotMask; };
         first = l.from[g];
         cnt = l.cnt[g];
-        const bool dp = cnt <= kDp4aTokens;
         b = row(int(l.ord[first + min(lane >> 2, cnt - 1)]));
-        s0 = row(int(l.ord[first + (dp ? 0 : min(2 * (lane & 3), cnt - 1))]));
-        s1 = row(int(l.ord[first + (dp ? cnt - 1 : min(2 * (lane & 3) + 1, cnt - 1))]));
+        s0 = row(int(l.ord[first + min(2 * (lane & 3), cnt - 1)]));
+        s1 = row(int(l.ord[first + min(2 * (lane & 3) + 1, cnt - 1)]));
     }
 };
 // Both forms' sums; the other one's stay zero.
 struct Sums {
     unsigned long long m[2][2];
-    float d[kDp4aTokens];
+    float d;
     __device__ __forceinline__ void clear() {
         m[0][0] = m[0][1] = m[1][0] = m[1][1] = 0ull;
-        d[0] = d[1] = 0.0f;
+        d = 0.0f;
     }
 };
 
@@ -606,7 +596,10 @@ __host__ __device__ __forceinline__ size_t gate_up_smem(int E, int n) {
 // CTAs. RG warps share a K slice's boxes (one per 16 gate and 16 up rows), 8 / RG slices; their
 // sums meet in shared memory, where a warp per token and 32 rows forms h, its block's scale
 // and codes. RG = 2 spreads few items over the GPU; RG = 4 (I a multiple of 64) halves what an
-// item costs beside its boxes.
+// item costs beside its boxes. Two CTAs per SM. 64 tokens, top 8 of 64 experts of 2048 x 1024:
+// 66 us for 151 MB, bound by instruction issue (32 M warp instructions, 0.52 per cycle and
+// scheduler); 4 tokens, top 2 of 8 experts of 4096 x 14336: 122 us for the whole layer, two
+// thirds of the copy rate, the rest uneven rounds of items.
 template <int RG>
 __global__ void __launch_bounds__(256, 2)
     gate_up_kernel(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* xq,
@@ -658,11 +651,10 @@ __global__ void __launch_bounds__(256, 2)
         const int r = int(l.act[gi]) * 2 * I + ir * ROWS + rg * 16;
         Group gr;
         gr.template set<true>(l, gi);
-        const bool dp = gr.cnt <= kDp4aTokens;
+        const bool one = gr.cnt == 1;
         const int pitch = Bp * 32;
-        const uint8_t* xb = xq + gr.b * pitch + (lane & 3) * 32;
+        const uint8_t* xb = xq + gr.b * pitch;
         const float *d0 = xd + gr.s0 * Bp, *d1 = xd + gr.s1 * Bp;
-        const uint8_t *t0 = xq + gr.s0 * pitch, *t1 = xq + gr.s1 * pitch;
         Sums acc;
         acc.clear();
 #pragma unroll 1
@@ -670,16 +662,11 @@ __global__ void __launch_bounds__(256, 2)
             const int st = ring.used % kStages;
             const uint32_t cq = ring.codes + st * kStageBytes;
             const uint8_t* cs = ring.scales + st * kScaleBytes;
-            if (dp) {
+            if (one) {
                 ring.wait(wd, sc_tma, j, r, r + I, B, &ctrl->abort);
-                const uint8_t* const x[2] = {t0 + j * 256, t1 + j * 256};
-                const float* const d[2] = {d0 + j * 8, d1 + j * 8};
-                if (gr.cnt == 1)
-                    stage_dp4a<false, 1>(acc.d, cq, cs, x, d);
-                else
-                    stage_dp4a<false, 2>(acc.d, cq, cs, x, d);
+                stage_dp4a<false>(acc.d, cq, cs, xb + j * 256, d0 + j * 8);
             } else {
-                const Frag f = load_frag<false>(xb + j * 256, d0 + j * 8, d1 + j * 8);
+                const Frag f = load_frag<false>(xb + (lane & 3) * 32 + j * 256, d0 + j * 8, d1 + j * 8);
                 ring.wait(wd, sc_tma, j, r, r + I, B, &ctrl->abort);
                 stage_mma(acc.m, cq, cs, f);
             }
@@ -688,10 +675,8 @@ __global__ void __launch_bounds__(256, 2)
             fetch();
         }
         float* p = red + ksl * 2 * ROWS * kRedPitch;  // gate rows, up rows
-        if (dp) {
-            float* q = p + ((lane >> 4) * ROWS + rg * 16 + (lane & 15)) * kRedPitch;
-            q[0] = acc.d[0];
-            q[1] = acc.d[1];
+        if (one) {
+            p[((lane >> 4) * ROWS + rg * 16 + (lane & 15)) * kRedPitch] = acc.d;
         } else {
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -746,6 +731,7 @@ __host__ __device__ __forceinline__ size_t down_smem(int T, int E, int n) {
 // for those rows are dealt in runs to the warps of the cluster; each warp adds its sums,
 // times the slots' weights, to a [token][row] array of its own, and the arrays are added in a
 // fixed order (within the CTA, then across the cluster through distributed shared memory).
+// 64 tokens, top 8 of 64 experts of 2048 x 1024: 51 us for 75 MB, bound by instruction issue.
 __global__ void __launch_bounds__(256, 2)
     down_kernel(int Tall, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* hq,
                 const float* hd, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_s,
@@ -807,14 +793,10 @@ __global__ void __launch_bounds__(256, 2)
     gr.cnt = 0;
     int a = -1;
     auto flush = [&]() {
-        if (gr.cnt <= kDp4aTokens) {
-#pragma unroll
-            for (int t = 0; t < kDp4aTokens; ++t)
-                if (t < gr.cnt) {
-                    const int entry = l.ord[gr.first + t];
-                    float* p = yw + (entry >> 10) * kYPitch + lane;
-                    *p = fmaf(l.w[entry & kSlotMask], acc.d[t], *p);
-                }
+        if (gr.cnt == 1) {
+            const int entry = l.ord[gr.first];
+            float* p = yw + (entry >> 10) * kYPitch + lane;
+            *p = fmaf(l.w[entry & kSlotMask], acc.d, *p);
         } else {
 #pragma unroll
             for (int col = 0; col < 2; ++col) {
@@ -833,7 +815,7 @@ __global__ void __launch_bounds__(256, 2)
         }
         __syncwarp();
     };
-    const uint8_t *xb = hq, *t0 = hq, *t1 = hq;
+    const uint8_t* xb = hq;
     const float *d0 = hd, *d1 = hd;
 #pragma unroll 1
     for (; left > 0; --left) {
@@ -841,9 +823,7 @@ __global__ void __launch_bounds__(256, 2)
             if (a >= 0) flush();
             a = ug;
             gr.template set<false>(l, a);
-            xb = hq + int64_t(gr.b) * pitch + (lane & 3) * 32;
-            t0 = hq + int64_t(gr.s0) * pitch;
-            t1 = hq + int64_t(gr.s1) * pitch;
+            xb = hq + int64_t(gr.b) * pitch;
             d0 = hd + int64_t(gr.s0) * Bp;
             d1 = hd + int64_t(gr.s1) * Bp;
             acc.clear();
@@ -853,16 +833,11 @@ __global__ void __launch_bounds__(256, 2)
         const int st = ring.used % kStages;
         const uint32_t cq = ring.codes + st * kStageBytes;
         const uint8_t* cs = ring.scales + st * kScaleBytes;
-        if (gr.cnt <= kDp4aTokens) {
+        if (gr.cnt == 1) {
             ring.wait(wd, sc_tma, j, r, r + 16, B, &ctrl->abort);
-            const uint8_t* const x[2] = {t0 + j * 256, t1 + j * 256};
-            const float* const d[2] = {d0 + j * 8, d1 + j * 8};
-            if (gr.cnt == 1)
-                stage_dp4a<true, 1>(acc.d, cq, cs, x, d);
-            else
-                stage_dp4a<true, 2>(acc.d, cq, cs, x, d);
+            stage_dp4a<true>(acc.d, cq, cs, xb + j * 256, d0 + j * 8);
         } else {
-            const Frag f = load_frag<true>(xb + j * 256, d0 + j * 8, d1 + j * 8);
+            const Frag f = load_frag<true>(xb + (lane & 3) * 32 + j * 256, d0 + j * 8, d1 + j * 8);
             ring.wait(wd, sc_tma, j, r, r + 16, B, &ctrl->abort);
             stage_mma(acc.m, cq, cs, f);
         }

@@ -102,10 +102,10 @@ w4a8_status run_experts(int T, int E, int H, int I, int top_k, const int* ids, c
     const int n = T * top_k, td = T < moe::kDownTokens ? T : moe::kDownTokens;
     const int64_t items = int64_t(moe::max_groups(E, n, moe::kGroup)) * (I / 32);
     const int64_t slots = int64_t(sm_count()) * 2;
-    // 64 rows per item where that still leaves every CTA two of them and the experts have a few
-    // tokens each, so that what an item costs beside its boxes counts (64 tokens, top 8 of 64:
-    // 112 -> 108 us; 4 tokens, top 2 of 8, where rounds of items count more: 117 -> 123)
-    auto* gate_up = I % 64 == 0 && items >= 4 * slots && n >= 2 * E ? moe::gate_up_kernel<4> : moe::gate_up_kernel<2>;
+    // 64 rows per item where that still leaves every CTA two of them, which halves what an item costs
+    // beside its boxes (64 tokens, top 8 of 64, 2048 x 1024: 108 us against 111 with 32 rows; 16 tokens
+    // 59.3 / 61.2; one token, with 8 experts' items: 17.0 / 16.0)
+    auto* gate_up = I % 64 == 0 && items >= 4 * slots ? moe::gate_up_kernel<4> : moe::gate_up_kernel<2>;
     cudaError_t e = smem_limit_once(gate_up,
                                     int(moe::gate_up_smem(moe::kMaxExperts, moe::kMaxTokens * moe::kMaxTopK)));
     if (e == cudaSuccess)
