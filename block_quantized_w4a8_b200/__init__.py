@@ -418,6 +418,14 @@ def _typed(t: torch.Tensor, dtypes, dev: int, need: int, name: str):
     return _ptr(t, dev, need, name)
 
 
+def _codes(q: torch.Tensor, N: int, K: int, dev: int):
+    """_typed of N x K e4m3 codes, which lie in rows of K."""
+    p = _typed(q, _CODES, dev, N * K, "q")
+    if q.shape[-1] != K:
+        raise ValueError(f"libw4a8: q has rows of {q.shape[-1]} codes; this call takes {K}")
+    return p
+
+
 # The epilogues without a bias: read by the library during the call only.
 _NO_BIAS = {torch.float32: None, torch.bfloat16: ctypes.byref(Epilogue(None, W4A8_F32, W4A8_BF16))}
 
@@ -453,12 +461,12 @@ def w4a8_gemm_fp8(x, q, s, y, ws, bias=None, stream=None) -> None:
     M, K = x.shape
     N = q.shape[0]
     dev = _device(x)
+    codes = _codes(q, N, K, dev)
     epi = _NO_BIAS.get(y.dtype) if bias is None else None
     if bias is not None or y.dtype not in _NO_BIAS:
         epi = ctypes.byref(_epilogue(bias, y, N, dev))
     _check("w4a8_gemm_fp8",
-           load_library().w4a8_gemm_fp8(M, N, K, _ptr(x, dev), _dtype(x),
-                                        _typed(q, _CODES, dev, N * K, "q"),
+           load_library().w4a8_gemm_fp8(M, N, K, _ptr(x, dev), _dtype(x), codes,
                                         _typed(s, _F32, dev, _fp8_scales(N, K), "s"),
                                         epi, _ptr(y, dev, M * N * y.element_size(), "y"),
                                         _ptr(ws, dev), ws.nbytes, _stream(stream)))
@@ -470,11 +478,17 @@ def w4a8_gemm_fp8_backward(dy, q, s, dx, ws, stream=None) -> None:
     K = dx.shape[1]
     dev = _device(dy)
     _check("w4a8_gemm_fp8_backward",
-           load_library().w4a8_gemm_fp8_backward(M, N, K, _ptr(dy, dev), _dtype(dy),
-                                                 _typed(q, _CODES, dev, N * K, "q"),
+           load_library().w4a8_gemm_fp8_backward(M, N, K, _ptr(dy, dev), _dtype(dy), _codes(q, N, K, dev),
                                                  _typed(s, _F32, dev, _fp8_scales(N, K), "s"),
                                                  _dtype(dx), _ptr(dx, dev, M * K * dx.element_size(), "dx"),
                                                  _ptr(ws, dev), ws.nbytes, _stream(stream)))
+
+
+def _router(wr: torch.Tensor, E: int, H: int, dev: int):
+    p = _ptr(wr, dev, E * H * wr.element_size(), "wr")
+    if wr.shape != (E, H):
+        raise ValueError(f"libw4a8: wr is {tuple(wr.shape)}; this call takes ({E}, {H})")
+    return p
 
 
 def w4a8_moe_route(x, wr, top_k: int, ids, weights, renorm: bool = True, stream=None) -> None:
@@ -485,7 +499,7 @@ def w4a8_moe_route(x, wr, top_k: int, ids, weights, renorm: bool = True, stream=
     n = T * top_k * 4
     _check("w4a8_moe_route",
            load_library().w4a8_moe_route(T, E, H, top_k, int(renorm), _ptr(x, dev), _dtype(x),
-                                         _ptr(wr, dev, E * H * wr.element_size(), "wr"), _dtype(wr),
+                                         _router(wr, E, H, dev), _dtype(wr),
                                          _typed(ids, _I32, dev, n, "ids"),
                                          _typed(weights, _F32, dev, n, "weights"),
                                          _stream(stream)))
@@ -501,8 +515,12 @@ def _experts(dev: int, H: int, gu_qs, gu_d, dn_qs, dn_d):
     E, I = gu_qs.shape[0], gu_qs.shape[1] // 2
     gq, gd = _q4_0_bytes(E * 2 * I, H)
     dq, dd = _q4_0_bytes(E * H, I)
-    return E, I, (_ptr(gu_qs, dev, gq, "gu_qs"), _ptr(gu_d, dev, gd, "gu_d"), _ptr(dn_qs, dev, dq, "dn_qs"),
-                  _ptr(dn_d, dev, dd, "dn_d"))
+    p = (_ptr(gu_qs, dev, gq, "gu_qs"), _ptr(gu_d, dev, gd, "gu_d"), _ptr(dn_qs, dev, dq, "dn_qs"),
+         _ptr(dn_d, dev, dd, "dn_d"))
+    if gu_qs.shape != (E, 2 * I, H // 2) or dn_qs.shape != (E, H, I // 2):
+        raise ValueError(f"libw4a8: experts of {tuple(gu_qs.shape)} and {tuple(dn_qs.shape)} codes; "
+                         f"this call takes (E, 2 I, {H} / 2) and (E, {H}, I / 2)")
+    return E, I, p
 
 
 def w4a8_moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, y, ws, stream=None) -> None:
@@ -529,7 +547,7 @@ def w4a8_moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k: int, ids, weight
     n = T * top_k * 4
     _check("w4a8_moe_layer_q4_0",
            load_library().w4a8_moe_layer_q4_0(T, E, H, I, top_k, int(renorm), _ptr(x, dev), _dtype(x),
-                                              _ptr(wr, dev, E * H * wr.element_size(), "wr"), _dtype(wr), *experts,
+                                              _router(wr, E, H, dev), _dtype(wr), *experts,
                                               _typed(ids, _I32, dev, n, "ids"),
                                               _typed(weights, _F32, dev, n, "weights"),
                                               _dtype(y), _ptr(y, dev, T * H * y.element_size(), "y"), _ptr(ws, dev),
@@ -638,19 +656,27 @@ def gemm_affine(x, q, s, b, group: int, path: int = PATH_AUTO, ws=None, stream=N
     return y
 
 
+# The helpers below allocate outputs and workspace on the stream that the call runs on, so that
+# memory freed on another stream is not reused under it.
 def quant_act_fp8(x: torch.Tensor, stream=None):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quant_act_fp8(x)
     M, K = x.shape
     q = x.new_empty((M, K), dtype=torch.float8_e4m3fn)
     s = x.new_empty((M, -(-K // 128)), dtype=torch.float32)
-    w4a8_quant_act_fp8(x, q, s, stream)
+    w4a8_quant_act_fp8(x, q, s)
     return q, s
 
 
 def pack_fp8(w: torch.Tensor, stream=None):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return pack_fp8(w)
     N, K = w.shape
     q = torch.empty(N, K, dtype=torch.float8_e4m3fn, device=w.device)
     s = torch.empty(-(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
-    w4a8_pack_fp8(w, q, s, stream)
+    w4a8_pack_fp8(w, q, s)
     return q, s
 
 
@@ -663,27 +689,36 @@ def fp8_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
 
 
 def gemm_fp8(x, q, s, bias=None, out_dtype=torch.float32, ws=None, stream=None):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gemm_fp8(x, q, s, bias, out_dtype, ws)
     M, K = x.shape
     N = q.shape[0]
     y = x.new_empty((M, N), dtype=out_dtype)
     ws = fp8_workspace(M, N, K, x.device) if ws is None else ws
-    w4a8_gemm_fp8(x, q, s, y, ws, bias, stream)
+    w4a8_gemm_fp8(x, q, s, y, ws, bias)
     return y
 
 
 def gemm_fp8_backward(dy, q, s, out_dtype=torch.float32, ws=None, stream=None):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gemm_fp8_backward(dy, q, s, out_dtype, ws)
     M, N = dy.shape
     K = q.shape[1]
     dx = dy.new_empty((M, K), dtype=out_dtype)
     ws = fp8_workspace(M, N, K, dy.device) if ws is None else ws
-    w4a8_gemm_fp8_backward(dy, q, s, dx, ws, stream)
+    w4a8_gemm_fp8_backward(dy, q, s, dx, ws)
     return dx
 
 
 def moe_route(x, wr, top_k: int, renorm: bool = True, stream=None):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_route(x, wr, top_k, renorm)
     ids = torch.empty(x.shape[0], top_k, dtype=torch.int32, device=x.device)
     weights = torch.empty(x.shape[0], top_k, dtype=torch.float32, device=x.device)
-    w4a8_moe_route(x, wr, top_k, ids, weights, renorm, stream)
+    w4a8_moe_route(x, wr, top_k, ids, weights, renorm)
     return ids, weights
 
 
@@ -696,22 +731,28 @@ def moe_workspace(T: int, E: int, H: int, I: int, top_k: int, device="cuda") -> 
 
 
 def moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, out_dtype=torch.float32, ws=None, stream=None):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, out_dtype, ws)
     T, H = x.shape
     y = x.new_empty((T, H), dtype=out_dtype)
     if ws is None:
         ws = moe_workspace(T, gu_qs.shape[0], H, gu_qs.shape[1] // 2, ids.shape[1], x.device)
-    w4a8_moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, y, ws, stream)
+    w4a8_moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, y, ws)
     return y
 
 
 def moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k: int, renorm: bool = True, out_dtype=torch.float32, ws=None,
                    stream=None):
     """(y, ids, weights) of the routed layer."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k, renorm, out_dtype, ws)
     T, H = x.shape
     ids = x.new_empty((T, top_k), dtype=torch.int32)
     weights = x.new_empty((T, top_k), dtype=torch.float32)
     y = x.new_empty((T, H), dtype=out_dtype)
     if ws is None:
         ws = moe_workspace(T, gu_qs.shape[0], H, gu_qs.shape[1] // 2, top_k, x.device)
-    w4a8_moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k, ids, weights, y, ws, renorm, stream)
+    w4a8_moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k, ids, weights, y, ws, renorm)
     return y, ids, weights

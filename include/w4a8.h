@@ -341,7 +341,7 @@ w4a8_status w4a8_pack_fp8(const void* w, w4a8_dtype dtype, int N, int K, uint8_t
  * result does not depend on scheduling.
  * Few rows of x run tiles of 128 columns by 16 to 64 rows, the contracted axis split over a
  * cluster; a handful (M <= 16 with few blocks per CTA) are quantised inside that kernel, and
- * the workspace is then only checked; from about 37 tiles of 256 x 256 on, CTA pairs.
+ * the workspace is then only checked; more such tiles of 64 rows than SMs run on CTA pairs.
  * ws : w4a8_fp8_workspace_bytes(M, N, K) bytes (serves both calls; query it with the device
  *      current), 16-byte aligned; contents ignored on entry, garbage afterwards. Calls that
  *      share a workspace must be ordered on one stream. Returns 0 for invalid sizes.

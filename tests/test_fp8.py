@@ -163,3 +163,13 @@ def test_binding_refuses_other_element_types(fake):  # noqa: F811
     with pytest.raises(ValueError, match="contiguous"):
         fn(**{**tensors, "x": torch.zeros(272, 3).T})
     assert fake.calls == []
+
+
+@pytest.mark.parametrize("which", [2, 3])
+def test_binding_refuses_codes_of_another_width(fake, which):  # noqa: F811
+    name, fn, tensors, _ = _tensors()[which]
+    q = tensors["q"]
+    tensors["q"] = torch.zeros(q.shape[0], q.shape[1] + 16, dtype=q.dtype)
+    with pytest.raises(ValueError, match="rows of"):
+        fn(**tensors)
+    assert not fake.calls

@@ -231,3 +231,40 @@ def test_side_streams_and_captured_graphs(M, N, K):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, w4a8.gemm_fp8(x, q, s))
+
+
+def test_helpers_on_a_stream_argument_keep_their_memory():
+    """Outputs and workspace of a call on another stream are not handed out again while it waits
+    there: the current stream allocates and fills memory of the same sizes meanwhile."""
+    M, N, K = 40, 384, 512
+    q, s, _, _ = weights(N, K, 17)
+    x, dy = rand((M, K), 18).cuda(), rand((M, N), 19).cuda()
+    E, H, I, k = 4, 512, 96, 2
+    gu, dn, wr = rand((E * 2 * I, H), 20).cuda(), rand((E * H, I), 21).cuda(), rand((E, H), 22).cuda()
+    gq, gd = (t.view(E, 2 * I, -1) for t in w4a8.pack_q4_0(gu))
+    dq, dd = (t.view(E, H, -1) for t in w4a8.pack_q4_0(dn))
+    ids, p = w4a8.moe_route(x, wr, k)
+
+    def calls(stream):
+        yield from w4a8.quant_act_fp8(x, stream=stream)
+        yield from w4a8.pack_fp8(x, stream=stream)
+        yield w4a8.gemm_fp8(x, q, s, stream=stream)
+        yield w4a8.gemm_fp8_backward(dy, q, s, stream=stream)
+        yield from w4a8.moe_route(x, wr, k, stream=stream)
+        yield w4a8.moe_q4_0(x, ids, p, gq, gd, dq, dd, stream=stream)
+        yield from w4a8.moe_layer_q4_0(x, wr, gq, gd, dq, dd, k, stream=stream)
+
+    want = list(calls(None))
+    sizes = {t.nbytes for t in want} | {w4a8.w4a8_fp8_workspace_bytes(M, N, K),
+                                        w4a8.w4a8_moe_workspace_bytes(M, E, H, I, k)}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    got, junk = [], []
+    for t in calls(side):
+        got.append(t)
+        junk += [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

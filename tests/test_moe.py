@@ -155,3 +155,15 @@ def test_binding_passes_exact_sizes_and_refuses_short_tensors(fake, case):  # no
     with pytest.raises(ValueError, match="contiguous"):
         fn(**{**tensors, "x": torch.zeros(64, 3).T}, **other)
     assert fake.calls == []
+
+
+@pytest.mark.parametrize("change", [dict(gu_qs=(4, 193, 32)), dict(gu_qs=(4, 192, 48)), dict(dn_qs=(4, 65, 48)),
+                                    dict(wr=(5, 64)), dict(wr=(4, 96))])
+def test_binding_refuses_tensors_that_do_not_fit_together(fake, change):  # noqa: F811
+    """Large enough, but of other rows, widths or experts than the call reads them with."""
+    name, fn, tensors, other, _ = _tensors()[2]
+    for key, shape in change.items():
+        tensors[key] = torch.zeros(*shape, dtype=tensors[key].dtype)
+    with pytest.raises(ValueError):
+        fn(**tensors, **other)
+    assert not fake.calls
