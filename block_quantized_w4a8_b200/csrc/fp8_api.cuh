@@ -15,7 +15,7 @@ w4a8_status check_fp8_dtype(w4a8_dtype dt) {
 // Quantises M rows of length L into codes of the given pitch and scales of the given
 // strides, in launches of less than 2^28 blocks.
 w4a8_status run_fp8_quant(const void* x, w4a8_dtype dt, int M, int L, int pitch, uint8_t* q, float* s, int64_t srow,
-                          int64_t sblk, cudaStream_t stream) {
+                          int64_t sblk, bool early, cudaStream_t stream) {
     const int chunk = int((int64_t(1) << 27) / fp8_blocks(L));
     const bool vec = L % 16 == 0;
     for (int m0 = 0; m0 < M; m0 += chunk) {
@@ -26,7 +26,7 @@ w4a8_status run_fp8_quant(const void* x, w4a8_dtype dt, int M, int L, int pitch,
         const dim3 grid(unsigned(cdiv(int64_t(mc) * fp8_blocks(L), 32)));
         auto* kernel = dt == W4A8_BF16 ? (vec ? fp8::quant_rows_kernel<true, true> : fp8::quant_rows_kernel<true, false>)
                                        : (vec ? fp8::quant_rows_kernel<false, true> : fp8::quant_rows_kernel<false, false>);
-        kernel<<<grid, 256, 0, stream>>>(xc, mc, L, pitch, qc, sc, srow, sblk);
+        kernel<<<grid, 256, 0, stream>>>(xc, mc, L, pitch, qc, sc, srow, sblk, early ? 1 : 0);
         const w4a8_status st = launch_status();
         if (st != W4A8_OK) return st;
     }
@@ -169,7 +169,7 @@ w4a8_status fp8_gemm_impl(int M, int N, int K, const void* in, w4a8_dtype dt, co
     if (!pair && fp8_fused(M, C, R))
         return dt == W4A8_BF16 ? launch_fp8_rows<16, TRANS, true, true>(M, C, R, tw, w, in, s, swcols, out, epi, stream)
                                : launch_fp8_rows<16, TRANS, true, false>(M, C, R, tw, w, in, s, swcols, out, epi, stream);
-    const w4a8_status st = run_fp8_quant(in, dt, M, R, w.pitch, w.q, w.s, 1, w.spitch, stream);
+    const w4a8_status st = run_fp8_quant(in, dt, M, R, w.pitch, w.q, w.s, 1, w.spitch, true, stream);
     if (st != W4A8_OK) return st;
     if (pair) return launch_fp8_pair<TRANS>(M, C, R, tw, w, s, swcols, out, epi, stream);
     switch (fp8_token_tile(M)) {
@@ -188,7 +188,7 @@ w4a8_status w4a8_quant_act_fp8(const void* x, w4a8_dtype dtype, int M, int K, ui
     if (!fp8_dims_ok(M, 1, K) || !x || !q || !s) return W4A8_ERR_INVALID_ARG;
     if (check_fp8_dtype(dtype) != W4A8_OK) return W4A8_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(q) || !aligned16(s)) return W4A8_ERR_MISALIGNED;
-    return run_fp8_quant(x, dtype, M, K, K, q, s, fp8_blocks(K), 1, stream);
+    return run_fp8_quant(x, dtype, M, K, K, q, s, fp8_blocks(K), 1, false, stream);
 }
 
 w4a8_status w4a8_pack_fp8(const void* w, w4a8_dtype dtype, int N, int K, uint8_t* q, float* s, cudaStream_t stream) {

@@ -77,13 +77,16 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 // element of 16 lanes: the kernel is bound by its instructions, not by the bytes, for bf16).
 // Codes at q[m * pitch + k] (pitch a multiple of 16; with a pitch beyond L the rest of the row's
 // last 16 are written with zeros), the scale of (row m, block b) at s[m * srow + b * sblk].
-// VEC: L a multiple of 16. One block per group of lanes (two or four were no faster). 2048 x 4096 bf16:
-// 4.8 us, 25 MB at 5.3 TB/s.
+// early: the next kernel may start while this one runs (the contraction of the same call, which
+// waits before it reads q and s). Not for a caller's q and s: those of one row are also a weight
+// of one row, and weights are read before that wait.
+// VEC: L a multiple of 16. One block per group of lanes (two or four were no faster). 2048 x 4096
+// bf16: 4.8 us, 25 MB at 5.3 TB/s.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const void* __restrict__ x, int M, int L, int pitch,
                                                          uint8_t* __restrict__ q, float* __restrict__ s, int64_t srow,
-                                                         int64_t sblk) {
-    pdl_launch_dependents();
+                                                         int64_t sblk, int early) {
+    if (early) pdl_launch_dependents();
     const uint32_t nb = uint32_t(L + kBlk - 1) / kBlk, n = uint32_t(M) * nb;  // n < 2^28 per launch
     const uint32_t i = blockIdx.x * 32u + (threadIdx.x >> 3);
     const int lane = threadIdx.x & 7;

@@ -268,3 +268,19 @@ def test_helpers_on_a_stream_argument_keep_their_memory():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("K", [128, 16384])
+def test_a_quantised_row_is_a_weight_of_one_row(K):
+    """The codes and scales of one activation row are those of a 1 x K weight, and a call that
+    reads them as its weight directly afterwards sees them complete."""
+    x, rows = rand((1, K), 23).cuda(), rand((8, K), 24).cuda()
+    want = [w4a8.gemm_fp8(x, *w4a8.pack_fp8(r[None])) for r in rows]
+    q, s = torch.zeros(1, K, dtype=torch.float8_e4m3fn, device="cuda"), torch.zeros(1, K // 128, device="cuda")
+    y, ws = [torch.empty(1, 1, device="cuda") for _ in range(8)], w4a8.fp8_workspace(1, 1, K)
+    torch.cuda.synchronize()
+    for i in range(8):
+        w4a8.w4a8_quant_act_fp8(rows[i][None], q, s)
+        w4a8.w4a8_gemm_fp8(x, q, s, y[i], ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y[i], want[i]) for i in range(8))
