@@ -74,12 +74,18 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
 }
 
 constexpr int kRouteCtas = 8;  // CTAs per token (the cluster)
+// Tokens from which the router keeps 4 steps of loads in flight per warp instead of 8, whose
+// registers leave two CTAs per SM (whole layers, 4 against 8: one token, 256 experts, H = 4096
+// 26.2 / 23.7 us; 4 tokens, 8 experts 121.8 / 121.2; 13 tokens, 11 experts 20.3 / 20.9; 64 tokens,
+// 64 experts 107.0 / 108.2; 64 tokens, 256 experts of 1024 x 256 61.0 / 68.9).
+constexpr int kShallowTokens = 8;
 
 // Grid: kRouteCtas CTAs (a cluster) per token. Every CTA quantises its share of the token's
 // blocks (xq != nullptr) and, with ROUTE, computes the logits of its experts, a warp each;
-// they meet in the first CTA's shared memory, where one warp takes the top_k. Bound by latency:
-// 64 tokens x 64 experts, H = 2048: 11.6 us alone; the experts' first weights load meanwhile.
-template <bool ROUTE, bool XB, bool WB>
+// they meet in the first CTA's shared memory, where one warp takes the top_k. Bound by latency,
+// not bytes: about a tenth of the 107 us of a layer of 64 tokens and 64 experts of 2048 x 1024.
+// DEEP: steps of 256 columns whose loads are in flight together per warp.
+template <bool ROUTE, bool XB, bool WB, int DEEP>
 __global__ void __launch_bounds__(256, 1) route_kernel(int E, int H, int top_k, int renorm, const void* __restrict__ x,
                                                     const void* __restrict__ wr, int* __restrict__ ids,
                                                     float* __restrict__ weights, uint8_t* __restrict__ xq,
@@ -94,7 +100,7 @@ __global__ void __launch_bounds__(256, 1) route_kernel(int E, int H, int top_k, 
         bool waited = false;
         for (int e = rank + kRouteCtas * warp; e < E; e += kRouteCtas * 8) {
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
+#pragma unroll DEEP
             for (int k = lane * 8; k < H; k += 256) {
                 float a[8], b[8];
                 load8f<XB>(x, int64_t(t) * H + k, a);

@@ -44,6 +44,12 @@ w4a8_status check_route(int T, int E, int H, int top_k, const void* x, w4a8_dtyp
     return W4A8_OK;
 }
 
+template <int DEEP>
+auto* route_of(bool xb, bool wb) {
+    return xb ? (wb ? moe::route_kernel<true, true, true, DEEP> : moe::route_kernel<true, true, false, DEEP>)
+              : (wb ? moe::route_kernel<true, false, true, DEEP> : moe::route_kernel<true, false, false, DEEP>);
+}
+
 // One launch: the router (wr != nullptr) and the Q8_0 form of x (xq != nullptr).
 w4a8_status run_route(int T, int E, int H, int top_k, int renorm, const void* x, w4a8_dtype xdt, const void* wr,
                       w4a8_dtype wdt, int* ids, float* weights, uint8_t* xq, float* xd, cudaStream_t stream) {
@@ -59,9 +65,8 @@ w4a8_status run_route(int T, int E, int H, int top_k, int renorm, const void* x,
     cfg.attrs = attr;
     cfg.numAttrs = wr ? 1 : 0;
     const bool xb = xdt == W4A8_BF16, wb = wdt == W4A8_BF16;
-    auto* kernel = !wr ? (xb ? moe::route_kernel<false, true, false> : moe::route_kernel<false, false, false>)
-                   : xb ? (wb ? moe::route_kernel<true, true, true> : moe::route_kernel<true, true, false>)
-                        : (wb ? moe::route_kernel<true, false, true> : moe::route_kernel<true, false, false>);
+    auto* kernel = !wr ? (xb ? moe::route_kernel<false, true, false, 1> : moe::route_kernel<false, false, false, 1>)
+                       : T >= moe::kShallowTokens ? route_of<4>(xb, wb) : route_of<8>(xb, wb);
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, E, H, top_k, renorm, x, wr, ids, weights, xq, xd));
 }
 
