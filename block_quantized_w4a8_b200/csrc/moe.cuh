@@ -553,14 +553,15 @@ __device__ __forceinline__ Ring make_ring(uint8_t* smem, Ctrl* ctrl) {
     r.dead = false;
     return r;
 }
-__device__ __forceinline__ void init_ctrl(Ctrl* ctrl, const CUtensorMap* tq, const CUtensorMap* ts) {
+// The scales' map is encoded, and so prefetched, only with sc_tma.
+__device__ __forceinline__ void init_ctrl(Ctrl* ctrl, const CUtensorMap* tq, const CUtensorMap* ts, int sc_tma) {
     if (threadIdx.x == 0) {
         for (int w = 0; w < kWarps; ++w)
             for (int s = 0; s < kStages; ++s) mbar_init(smem_addr(&ctrl->full[w][s]), 1);
         ctrl->abort = 0;
         mbar_init_fence();
         asm volatile("prefetch.tensormap [%0];" ::"l"(tq) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(ts) : "memory");
+        if (sc_tma) asm volatile("prefetch.tensormap [%0];" ::"l"(ts) : "memory");
     }
 }
 
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(256, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int SLICES = kWarps / RG, ROWS = 16 * RG;
     const int rg = warp % RG, ksl = warp / RG;
-    init_ctrl(ctrl, &tm_q, &tm_s);
+    init_ctrl(ctrl, &tm_q, &tm_s, sc_tma);
     pdl_wait_primary();  // ids, xq and xd are written by the preceding kernel
     pdl_launch_dependents();
     build_lists(l, ids, weights, n, top_k, E, kGroup);
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(256, 2)
     const Lists l = lists_at(reinterpret_cast<uint8_t*>(ybuf + kWarps * YT), smem, E, n, kGroup);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n0 = blockIdx.y * 32, slices = gridDim.x * kWarps;
-    init_ctrl(ctrl, &tm_q, &tm_s);
+    init_ctrl(ctrl, &tm_q, &tm_s, sc_tma);
     for (int i = threadIdx.x; i < kWarps * YT; i += 256) ybuf[i] = 0.0f;
     // Read before the wait: ids and weights come from the kernel before the preceding one,
     // which has completed, since every CTA of the preceding kernel waits for it before it

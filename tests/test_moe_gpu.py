@@ -90,6 +90,13 @@ def test_experts_with_exact_gate_and_up(T, E, H, I, k):
     check(y, yref, bound + TOL * A)
 
 
+@pytest.mark.parametrize("T", [1, 20])
+@pytest.mark.parametrize("H,I", [(256, 256), (256, 288), (288, 256), (288, 288)])
+def test_scale_rows_with_and_without_a_tensor_map(T, H, I):
+    """Scale rows of 16-byte units come by TMA, others by plain loads; each product for itself."""
+    verify(*make(T, 4, H, I, 2, H + 2 * I + T), torch.float32, TOL)
+
+
 def test_empty_slots_repeated_experts_and_empty_tokens():
     T, E, H, I, k = 6, 5, 256, 96, 3
     x, gu, dn, ids, weights = make(T, E, H, I, k, 3)
