@@ -22,6 +22,7 @@
 #include <cuda.h>
 
 #include "device_common.cuh"
+#include "ring_count.cuh"
 
 namespace w4a8 {
 namespace moe {
@@ -346,7 +347,6 @@ __device__ __forceinline__ void build_lists(const Lists& l, const int* ids, cons
 // ------------------------------------------------------------------ the stream
 constexpr int kWarps = 8;
 constexpr int kGroup = 8;          // tokens of a group: the MMA's columns
-constexpr int kStages = 2;
 constexpr int kBoxBlocks = 8;      // quant blocks per box
 constexpr int kTileBytes = 2048;   // 16 rows x 8 blocks of codes, 128-byte swizzle
 constexpr int kStageBytes = 2 * kTileBytes;
@@ -354,15 +354,13 @@ constexpr int kScaleBytes = 512;   // 2 x 16 rows x 8 fp16
 constexpr int kRingBytes = kWarps * kStages * (kStageBytes + kScaleBytes);
 
 // One warp's ring: two 16-row tiles of 8 blocks per stage.
-struct Ring {
+struct Ring : RingCount {
     uint32_t codes, bars;  // shared addresses of this warp's stages and barriers
     uint8_t* scales;
-    int issued, used;
-    bool dead;             // a wait ran out: nothing more is issued or waited for
 
     // Lane 0 of the warp: fetch box j of the rows r0 .. r0+15 and r1 .. r1+15.
     __device__ __forceinline__ void issue(const CUtensorMap* tq, const CUtensorMap* ts, int sc_tma, int j, int r0, int r1) {
-        const int st = issued % kStages;
+        const int st = stage(issued);
         const uint32_t bar = bars + st * 8, q = codes + st * kStageBytes;
         mbar_arrive_expect_tx(bar, kStageBytes + (sc_tma ? kScaleBytes : 0));
         tma_load_2d<1>(q, tq, j * 128, r0, bar);
@@ -376,7 +374,7 @@ struct Ring {
     // Wait for the next box. Without sc_tma (scale rows whose pitch is not a multiple of 16
     // bytes) the warp fetches the box's scales itself, zeros past the row.
     __device__ __forceinline__ void wait(const uint16_t* wd, int sc_tma, int j, int r0, int r1, int B, volatile uint32_t* abort) {
-        const int st = used % kStages, lane = threadIdx.x & 31;
+        const int st = stage(used), lane = threadIdx.x & 31;
         if (!sc_tma) {
             uint32_t h[4] = {0u, 0u, 0u, 0u};
             const uint16_t* src = wd + int64_t((lane < 16 ? r0 : r1) + (lane & 15)) * B + j * kBoxBlocks;
@@ -386,10 +384,10 @@ struct Ring {
             *reinterpret_cast<uint4*>(scales + st * kScaleBytes + lane * 16) = make_uint4(h[0], h[1], h[2], h[3]);
             __syncwarp();
         }
-        if (!dead && !bounded_wait_warp(bars + st * 8, (used / kStages) & 1, abort)) dead = true;
+        if (!dead && !bounded_wait_warp(bars + st * 8, parity(used), abort)) dead = true;
     }
     __device__ __forceinline__ void drain() {
-        for (int i = used; i < issued; ++i) drain_wait_warp(bars + (i % kStages) * 8, (i / kStages) & 1, 200000ull);
+        for (int i = first_pending(); i < issued; ++i) drain_wait_warp(bars + stage(i) * 8, parity(i), 200000ull);
     }
 };
 
@@ -549,8 +547,7 @@ __device__ __forceinline__ Ring make_ring(uint8_t* smem, Ctrl* ctrl) {
     r.codes = smem_addr(smem) + uint32_t(warp * kStages * kStageBytes);
     r.scales = smem + kWarps * kStages * kStageBytes + warp * kStages * kScaleBytes;
     r.bars = smem_addr(&ctrl->full[warp][0]);
-    r.issued = r.used = 0;
-    r.dead = false;
+    r.reset();
     return r;
 }
 // The scales' map is encoded, and so prefetched, only with sc_tma.
@@ -666,7 +663,7 @@ __global__ void __launch_bounds__(256, 2)
         acc.clear();
 #pragma unroll 1
         for (int j = ksl; j < nbox; j += SLICES) {
-            const int st = ring.used % kStages;
+            const int st = Ring::stage(ring.used);
             const uint32_t cq = ring.codes + st * kStageBytes;
             const uint8_t* cs = ring.scales + st * kScaleBytes;
             if (one) {
@@ -837,7 +834,7 @@ __global__ void __launch_bounds__(256, 2)
         }
         const int r = int(l.act[ug]) * H + n0, j = uj;
         step(ug, uj);
-        const int st = ring.used % kStages;
+        const int st = Ring::stage(ring.used);
         const uint32_t cq = ring.codes + st * kStageBytes;
         const uint8_t* cs = ring.scales + st * kScaleBytes;
         if (gr.cnt == 1) {

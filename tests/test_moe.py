@@ -1,6 +1,8 @@
 """Host side of the mixture-of-experts layer (no GPU): the reference the GPU tests use,
 refusals with the documented status codes, workspace sizes, and the binding's checks."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -64,6 +66,51 @@ def test_reference_layer_is_the_plain_formula_up_to_its_bound():
             slack += w[t, s] * np.abs(dn[ids[t, s]]) @ (step / 2)
         assert np.all(np.abs(y[t] - want) <= slack * (1 + 1e-6) + bound[t])
     assert np.all(bound < 1e-3 * np.abs(y).max() + 1e-9)  # with exact dots almost nothing may flip
+
+
+# ------------------------------------------------------------------ copies in flight
+RING_SIM = """
+#include <cstdio>
+#include <set>
+#include "ring_count.cuh"
+using w4a8::moe::RingCount;
+// A warp's loop over n boxes, as the expert kernels run it: two requests ahead, then wait,
+// read, count, request. The wait for box `lost` runs out (lost = n: none does).
+int main() {
+    for (int n = 0; n < 12; ++n)
+        for (int lost = 0; lost <= n; ++lost) {
+            RingCount r;
+            r.reset();
+            std::set<int> flight;
+            auto fetch = [&] {
+                if (r.issued == n || r.dead) return;
+                for (int f : flight)
+                    if (RingCount::stage(f) == RingCount::stage(r.issued)) return (void)std::printf("overrun\\n");
+                flight.insert(r.issued++);
+            };
+            fetch();
+            fetch();
+            for (int box = 0; box < n; ++box) {
+                if (box == lost) r.dead = true;
+                if (!r.dead) flight.erase(r.used);
+                ++r.used;
+                fetch();
+            }
+            for (int i = r.first_pending(); i < r.issued; ++i) flight.erase(i);  // the drain
+            if (!flight.empty()) std::printf("n %d lost %d: %zu in flight at the end\\n", n, lost, flight.size());
+        }
+}
+"""
+
+
+def test_no_copy_is_left_in_flight_after_a_wait_that_ran_out(tmp_path):
+    """A block that ends while a copy into its shared memory is in flight may overwrite its
+    successor's: whatever the box whose wait runs out, the drain covers what was requested."""
+    src, exe = tmp_path / "ring.cpp", tmp_path / "ring"
+    src.write_text(RING_SIM)
+    csrc = os.path.join(os.path.dirname(w4a8.__file__), "csrc")
+    subprocess.check_call(["g++", "-std=c++17", "-x", "c++", "-I", csrc, str(src), "-o", str(exe)])
+    assert subprocess.check_output([str(exe)], text=True) == ""
 
 
 # ------------------------------------------------------------------ the C ABI's refusals
