@@ -130,7 +130,10 @@ __global__ void __launch_bounds__(256, 1) route_kernel(int E, int H, int top_k, 
             float v[4] = {0.f, 0.f, 0.f, 0.f};
             if (b < B) load4<XB>(x, int64_t(t) * H + b * 32 + sub * 4, v);
             const float amax = warp_max8(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
-            const float d = __fdiv_rn(amax, 127.0f);
+            // the maximum passes over a NaN, whose code is 0: the block's scale carries it on
+            const uint32_t nans = __ballot_sync(0xffffffffu, v[0] != v[0] || v[1] != v[1] || v[2] != v[2] || v[3] != v[3]);
+            const bool nan = (nans >> (threadIdx.x & 24u)) & 0xFFu;
+            const float d = nan ? __int_as_float(0x7FC00000) : __fdiv_rn(amax, 127.0f);
             const float id = d != 0.0f ? __frcp_rn(d) : 0.0f;
             uint32_t w = 0;
 #pragma unroll

@@ -366,9 +366,9 @@ w4a8_status w4a8_gemm_fp8_backward(int M, int N, int K, const void* dy, w4a8_dty
  *  w4a8_moe_q4_0       : y[t] = sum_s weights[t][s] * down(e), e = ids[t][s], with
  *                          g = xq . Wg[e]^T, u = xq . Wu[e]^T   (as w4a8_gemm, xq = Q8_0(x[t]))
  *                          h = g / (1 + exp(-g)) * u            (f32)
- *                          down(e) = hq . Wd[e]^T               (hq = Q8_0(h); a NaN in h makes
- *                                                                the token's row NaN)
- *                        A slot whose id is negative or not below E is empty and adds
+ *                          down(e) = hq . Wd[e]^T               (hq = Q8_0(h))
+ *                        A NaN in x[t], or in an h of the token, makes the token's row NaN: its
+ *                        block of xq or hq gets a NaN scale. A slot whose id is negative or not below E is empty and adds
  *                        nothing (a token with only empty slots gets a row of zeros); an
  *                        expert named by two slots of a token counts with the sum of their weights.
  *  w4a8_moe_layer_q4_0 : both; writes ids and weights too.

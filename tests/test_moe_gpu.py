@@ -134,6 +134,26 @@ def test_nan_in_h_reaches_its_token_and_no_other(T):
     assert torch.equal(z[1:], y[1:])
 
 
+@pytest.mark.parametrize("T", [1, 2, 12, 40])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("k0", [0, 45, 287])
+def test_nan_in_x_reaches_its_token_and_no_other(T, dtype, k0):
+    """With the caller's ids and weights: the row is NaN whichever element of whichever block is, the
+    others keep every bit, and a token without an expert stays zero."""
+    E, H, I, k = 2, 288, 96, 2
+    x, gu, dn, ids, weights = make(T, E, H, I, k, 7, dtype)
+    y = run(x, gu, dn, ids, weights)
+    for t in {0, T - 1}:
+        bad = x.clone()
+        bad[t, k0] = float("nan")
+        z = run(bad, gu, dn, ids, weights)
+        rest = [i for i in range(T) if i != t]
+        assert torch.isnan(z[t]).all() and torch.equal(z[rest], y[rest])
+        none = ids.clone()
+        none[t] = -1
+        assert torch.equal(run(bad, gu, dn, none, weights)[t], torch.zeros(H, device="cuda"))
+
+
 def test_a_token_does_not_depend_on_the_others():
     """Each token alone gives what it gives in the batch (up to the order of its sums); other
     values in the neighbours' rows, NaN among them, do not change a bit."""
