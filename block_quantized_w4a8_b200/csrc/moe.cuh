@@ -351,6 +351,7 @@ __device__ __forceinline__ void build_lists(const Lists& l, const int* ids, cons
 constexpr int kWarps = 8;
 constexpr int kGroup = 8;          // tokens of a group: the MMA's columns
 constexpr int kBoxBlocks = 8;      // quant blocks per box
+constexpr int kChainBoxes = 16;    // boxes added to one f32 sum (128 blocks, as w4a8_gemm); sums of longer runs are added up
 constexpr int kTileBytes = 2048;   // 16 rows x 8 blocks of codes, 128-byte swizzle
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kScaleBytes = 512;   // 2 x 16 rows x 8 fp16
@@ -663,35 +664,42 @@ __global__ void __launch_bounds__(256, 2)
         const uint8_t* xb = xq + gr.b * pitch;
         const float *d0 = xd + gr.s0 * Bp, *d1 = xd + gr.s1 * Bp;
         Sums acc;
-        acc.clear();
-#pragma unroll 1
-        for (int j = ksl; j < nbox; j += SLICES) {
-            const int st = Ring::stage(ring.used);
-            const uint32_t cq = ring.codes + st * kStageBytes;
-            const uint8_t* cs = ring.scales + st * kScaleBytes;
-            if (one) {
-                ring.wait(wd, sc_tma, j, r, r + I, B, &ctrl->abort);
-                stage_dp4a<false>(acc.d, cq, cs, xb + j * 256, d0 + j * 8);
-            } else {
-                const Frag f = load_frag<false>(xb + (lane & 3) * 32 + j * 256, d0 + j * 8, d1 + j * 8);
-                ring.wait(wd, sc_tma, j, r, r + I, B, &ctrl->abort);
-                stage_mma(acc.m, cq, cs, f);
-            }
-            __syncwarp();
-            ++ring.used;
-            fetch();
-        }
         float* p = red + ksl * 2 * ROWS * kRedPitch;  // gate rows, up rows
-        if (one) {
-            p[((lane >> 4) * ROWS + rg * 16 + (lane & 15)) * kRedPitch] = acc.d;
-        } else {
+        int j = ksl;
+#pragma unroll 1
+        for (bool first = true; first || j < nbox; first = false) {
+            const int end = min(nbox, j + SLICES * kChainBoxes);
+            acc.clear();
+#pragma unroll 1
+            for (; j < end; j += SLICES) {
+                const int st = Ring::stage(ring.used);
+                const uint32_t cq = ring.codes + st * kStageBytes;
+                const uint8_t* cs = ring.scales + st * kScaleBytes;
+                if (one) {
+                    ring.wait(wd, sc_tma, j, r, r + I, B, &ctrl->abort);
+                    stage_dp4a<false>(acc.d, cq, cs, xb + j * 256, d0 + j * 8);
+                } else {
+                    const Frag f = load_frag<false>(xb + (lane & 3) * 32 + j * 256, d0 + j * 8, d1 + j * 8);
+                    ring.wait(wd, sc_tma, j, r, r + I, B, &ctrl->abort);
+                    stage_mma(acc.m, cq, cs, f);
+                }
+                __syncwarp();
+                ++ring.used;
+                fetch();
+            }
+            // into this warp's words of the sums, each always the same lane's
+            auto put = [&](float* q, float v) { *q = first ? v : __fadd_rn(*q, v); };
+            if (one) {
+                put(p + ((lane >> 4) * ROWS + rg * 16 + (lane & 15)) * kRedPitch, acc.d);
+            } else {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                float a, b;
-                unpack2(acc.m[m >> 1][m & 1], a, b);
-                float* q = p + ((m >> 1) * ROWS + rg * 16 + (m & 1) * 8 + (lane >> 2)) * kRedPitch + 2 * (lane & 3);
-                q[0] = a;
-                q[1] = b;
+                for (int m = 0; m < 4; ++m) {
+                    float a, b;
+                    unpack2(acc.m[m >> 1][m & 1], a, b);
+                    float* q = p + ((m >> 1) * ROWS + rg * 16 + (m & 1) * 8 + (lane >> 2)) * kRedPitch + 2 * (lane & 3);
+                    put(q, a);
+                    put(q + 1, b);
+                }
             }
         }
         __syncthreads();
@@ -769,16 +777,10 @@ __global__ void __launch_bounds__(256, 2)
     const int nact = *l.nact;
     Ring ring = make_ring(smem, ctrl);
     // this warp's boxes of all groups' boxes in order: one run, so that a group's sums are
-    // flushed once per warp that meets it
+    // flushed once per warp that meets it (and every kChainBoxes boxes)
     const int64_t total = int64_t(nact) * nbox, s = blockIdx.x * kWarps + warp;
     int left = int((s + 1) * total / slices - s * total / slices), pleft = left;
     int pg = int(s * total / slices / nbox), pj = int(s * total / slices - int64_t(pg) * nbox);  // the next box to fetch
-    auto step = [&](int& g, int& j) {
-        if (++j == nbox) {
-            j = 0;
-            ++g;
-        }
-    };
     auto fetch = [&]() {
         if (pleft == 0 || ring.dead) return;
         if (lane == 0) {
@@ -787,7 +789,10 @@ __global__ void __launch_bounds__(256, 2)
         }
         ++ring.issued;
         --pleft;
-        step(pg, pj);
+        if (++pj == nbox) {
+            pj = 0;
+            ++pg;
+        }
     };
     int ug = pg, uj = pj;  // the box in hand
     fetch();
@@ -797,8 +802,6 @@ __global__ void __launch_bounds__(256, 2)
     float* yw = ybuf + warp * YT;
     Sums acc;
     Group gr;
-    gr.cnt = 0;
-    int a = -1;
     auto flush = [&]() {
         if (gr.cnt == 1) {
             const int entry = l.ord[gr.first];
@@ -822,37 +825,38 @@ __global__ void __launch_bounds__(256, 2)
         }
         __syncwarp();
     };
-    const uint8_t* xb = hq;
-    const float *d0 = hd, *d1 = hd;
 #pragma unroll 1
-    for (; left > 0; --left) {
-        if (ug != a) {
-            if (a >= 0) flush();
-            a = ug;
-            gr.template set<false>(l, a);
-            xb = hq + int64_t(gr.b) * pitch;
-            d0 = hd + int64_t(gr.s0) * Bp;
-            d1 = hd + int64_t(gr.s1) * Bp;
-            acc.clear();
+    while (left > 0) {  // the run's part in one group, at most kChainBoxes boxes at a time
+        const int end = min(uj + min(left, kChainBoxes), nbox);
+        left -= end - uj;
+        gr.template set<false>(l, ug);
+        const uint8_t* xb = hq + int64_t(gr.b) * pitch;
+        const float *d0 = hd + int64_t(gr.s0) * Bp, *d1 = hd + int64_t(gr.s1) * Bp;
+        const int r = int(l.act[ug]) * H + n0;
+        acc.clear();
+#pragma unroll 1
+        for (; uj < end; ++uj) {
+            const int st = Ring::stage(ring.used);
+            const uint32_t cq = ring.codes + st * kStageBytes;
+            const uint8_t* cs = ring.scales + st * kScaleBytes;
+            if (gr.cnt == 1) {
+                ring.wait(wd, sc_tma, uj, r, r + 16, B, &ctrl->abort);
+                stage_dp4a<true>(acc.d, cq, cs, xb + uj * 256, d0 + uj * 8);
+            } else {
+                const Frag f = load_frag<true>(xb + (lane & 3) * 32 + uj * 256, d0 + uj * 8, d1 + uj * 8);
+                ring.wait(wd, sc_tma, uj, r, r + 16, B, &ctrl->abort);
+                stage_mma(acc.m, cq, cs, f);
+            }
+            __syncwarp();
+            ++ring.used;
+            fetch();
         }
-        const int r = int(l.act[ug]) * H + n0, j = uj;
-        step(ug, uj);
-        const int st = Ring::stage(ring.used);
-        const uint32_t cq = ring.codes + st * kStageBytes;
-        const uint8_t* cs = ring.scales + st * kScaleBytes;
-        if (gr.cnt == 1) {
-            ring.wait(wd, sc_tma, j, r, r + 16, B, &ctrl->abort);
-            stage_dp4a<true>(acc.d, cq, cs, xb + j * 256, d0 + j * 8);
-        } else {
-            const Frag f = load_frag<true>(xb + (lane & 3) * 32 + j * 256, d0 + j * 8, d1 + j * 8);
-            ring.wait(wd, sc_tma, j, r, r + 16, B, &ctrl->abort);
-            stage_mma(acc.m, cq, cs, f);
+        flush();
+        if (uj == nbox) {
+            uj = 0;
+            ++ug;
         }
-        __syncwarp();
-        ++ring.used;
-        fetch();
     }
-    if (a >= 0) flush();
     ring.drain();
     __syncthreads();
     for (int i = threadIdx.x; i < T * 32; i += 256) {

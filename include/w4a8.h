@@ -379,9 +379,11 @@ w4a8_status w4a8_gemm_fp8_backward(int M, int N, int K, const void* dy, w4a8_dty
  * ws          : w4a8_moe_workspace_bytes bytes, 16-byte aligned; contents ignored on entry,
  *               garbage afterwards. Calls that share one must be ordered on one stream.
  *               Returns 0 for sizes the calls refuse.
- * Every dot is within 1e-5 * sum |block terms| of the exact one, as w4a8_gemm; a value of h so
- * close to a rounding border that this error carries it across changes by one step of its
- * block. A call's result does not depend on scheduling; the order of a token's sum over
+ * Every dot is within 1e-5 * sum |block terms| of the exact one for H and I up to 65536, as
+ * w4a8_gemm (no f32 chain is longer than 128 blocks), and within (150 + width / 4096) * 2^-24 *
+ * sum |block terms| beyond; the sum over a token's slots adds at most I / 4096 + 2 roundings of f32 per slot.
+ * A value of h so close to a rounding border that this error carries it across changes by one
+ * step of its block. A call's result does not depend on scheduling; the order of a token's sum over
  * experts may depend on which other experts the batch uses.
  * Limits: T <= W4A8_MOE_MAX_TOKENS (the routed calls), E <= W4A8_MOE_MAX_EXPERTS, top_k <=
  * min(E, W4A8_MOE_MAX_TOPK), I <= W4A8_MAX_DIM / 2; H and I multiples of 32.

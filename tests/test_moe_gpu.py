@@ -181,6 +181,58 @@ def test_large_and_zero_gates():
     assert torch.all(y[1] == 0)
 
 
+def dot_error(width):
+    """What a dot may be off by, relative to the sum of its terms' magnitudes."""
+    return max(TOL, (150 + width / 4096) * 2.0 ** -24)
+
+
+def equal_terms(T, E, H, I, k, dg, du, dd, x, used):
+    """(y / expected - 1) of the used tokens, where all weight codes are 7, all scales of a kind equal and
+    every token's elements equal: all block terms of a dot are one number, so the roundings of a long
+    sum add up instead of averaging out. Expected: from the definition in 64 bits."""
+    f16 = lambda rows, K, v: torch.full((E, rows, K // 32), v, dtype=torch.float16, device="cuda")
+    code = lambda rows, K: torch.full((E, rows, K // 2), 0xFF, dtype=torch.uint8, device="cuda")
+    gd = f16(2 * I, H, dg)
+    gd[:, I:] = du
+    dg, du, dd = (float(torch.tensor(v, dtype=torch.float16)) for v in (dg, du, dd))
+    ids = torch.full((T, k), -1, dtype=torch.int32)
+    ids[:used] = torch.arange(k, dtype=torch.int32)
+    xs = np.resize(np.asarray(x, dtype=np.float32), used)
+    full = torch.zeros(T, H)
+    full[:used] = torch.from_numpy(xs)[:, None]
+    y = w4a8.moe_q4_0(full.cuda(), ids.cuda(), torch.ones(T, k, device="cuda"), code(2 * I, H), gd.view(torch.int16),
+                      code(H, I), f16(H, I, dd).view(torch.int16))
+    assert w4a8.w4a8_last_device_error() == 0 and torch.all(y[used:] == 0)
+    xv = (xs / np.float32(127)).astype(np.float64) * 127  # amax / 127, every code 127
+    g, u = 7 * dg * xv * H, 7 * du * xv * H
+    want = k * 7 * dd * I * (g / (1 + np.exp(-g)) * u)
+    return np.abs(y[:used].cpu().numpy().astype(np.float64) / want[:, None] - 1).max()
+
+
+@pytest.mark.parametrize("T,E,H,I,k", [(1, 1, 1 << 18, 32, 1), (7, 1, 1 << 18, 32, 1), (64, 16, 1 << 17, 320, 16)])
+@pytest.mark.parametrize("dg", [0.0011, 0.0007, 0.00053, 0.0019])
+def test_long_sums_in_gate_and_up(T, E, H, I, k, dg):
+    """g = u, so h errs by twice a dot's error (g / silu(g) * silu'(g) - 1 < 1e-7 for g >= 20). Besides: 32
+    steps of 2^-24 for exp, division, products, the scale of h and down's sum of I / 32 <= 10 terms, and
+    the weighted sum's 3 per slot."""
+    worst = max(equal_terms(T, E, H, I, k, dg, dg, 0.0005, (20 + 1.7 * np.arange(7) + off) / (7 * dg * H), T)
+                for off in (0.0, 0.61, 1.13))
+    assert worst <= 2 * dot_error(H) + (32 + 3 * k) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("T,E,H,I,k,used", [(40, 1, 2432, 1 << 17, 1, 40), (33, 8, 2432, 1 << 16, 8, 1)])
+def test_long_sums_in_down(T, E, H, I, k, used):
+    """x = 127 * 2^-a and scales of g and u of one and of four bits: their sums are exact (multiples of
+    one unit, below 2^24 of it: 889 * 15 * 76). So only the down product's sum errs beside the 32 steps above
+    and the order in which a token's slots are added, I / 4096 + 2 steps per slot. A grid of one
+    CTA per tile (H / 32 * ceil(T / 32) > 148), whose warps take the longest runs of boxes."""
+    worst = 0.0
+    for dd in (0.0011, 0.0007, 0.00053, 0.0019, 0.00131, 0.00087):
+        for du in (1.25, 1.875):
+            worst = max(worst, equal_terms(T, E, H, I, k, 2.0 ** -10, du * 2.0 ** -10, dd, 127 * 2.0 ** -np.array([6, 7]), used))
+    assert worst <= dot_error(I) + (32 + k * (I / 4096 + 2)) * 2.0 ** -24
+
+
 # ------------------------------------------------------------------ router
 @pytest.mark.parametrize("T,E,H,k", [(1, 1, 32, 1), (3, 8, 96, 2), (5, 11, 1504, 3), (64, 64, 2048, 8), (2, 256, 512, 16),
                                      (300, 7, 256, 7)])
