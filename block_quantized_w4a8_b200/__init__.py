@@ -13,6 +13,7 @@ allocate the outputs and the workspace with torch and then call the same entry p
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -137,7 +138,7 @@ def _ptr(t: torch.Tensor | None, dev: int, need: int = 0, name: str = "tensor"):
         raise ValueError(f"libw4a8: {name} is not on the call's device")
     if not t.is_contiguous():
         raise ValueError(f"libw4a8 takes contiguous tensors ({name})")
-    if t.nbytes < need:
+    if need and t.nbytes < need:
         raise ValueError(f"libw4a8: {name} holds {t.nbytes} bytes; this call uses {need}")
     return ctypes.c_void_p(t.data_ptr())
 
@@ -418,11 +419,48 @@ def _typed(t: torch.Tensor, dtypes, dev: int, need: int, name: str):
     return _ptr(t, dev, need, name)
 
 
-def _codes(q: torch.Tensor, N: int, K: int, dev: int):
-    """_typed of N x K e4m3 codes, which lie in rows of K."""
-    p = _typed(q, _CODES, dev, N * K, "q")
+# Tensors of exactly the shape their call names hold its bytes in its order: the checks below look
+# further only at others. Outputs may be buffers of more rows, or flat; one of other rows has the
+# bytes, but in another order. Weights have to be of just their shapes (scales may be flat).
+def _rows(t: torch.Tensor, width: int, name: str) -> None:
+    if t.dim() > 1 and t.shape[-1] != width:
+        raise ValueError(f"libw4a8: {name} has rows of {t.shape[-1]}; this call takes {width}")
+
+
+def _fits(t: torch.Tensor, shape, name: str) -> None:
+    if t.shape != shape:
+        raise ValueError(f"libw4a8: {name} is {tuple(t.shape)}; this call takes {shape}")
+
+
+def _out(t: torch.Tensor, rows: int, width: int, dev: int, name: str):
+    """_ptr of a (rows, width) output in its own element type."""
+    if t.shape == (rows, width):
+        return _ptr(t, dev, 0, name)
+    p = _ptr(t, dev, rows * width * t.element_size(), name)
+    _rows(t, width, name)
+    return p
+
+
+def _typed_out(t: torch.Tensor, dtypes, rows: int, width: int, dev: int, name: str):
+    """_ptr of a (rows, width) tensor whose element type the call fixes."""
+    if t.shape == (rows, width):
+        return _typed(t, dtypes, dev, 0, name)
+    p = _typed(t, dtypes, dev, rows * width * t.element_size(), name)
+    _rows(t, width, name)
+    return p
+
+
+def _fp8_weight(q: torch.Tensor, s: torch.Tensor, N: int, K: int, dev: int):
+    """Pointers of an N x K weight's codes and scales."""
+    scales = (-(-N // 128), -(-K // 128))
+    if q.shape == (N, K) and s.shape == scales:
+        return _typed(q, _CODES, dev, 0, "q"), _typed(s, _F32, dev, 0, "s")
+    p = _typed(q, _CODES, dev, N * K, "q"), _typed(s, _F32, dev, _fp8_scales(N, K), "s")
     if q.shape[-1] != K:
         raise ValueError(f"libw4a8: q has rows of {q.shape[-1]} codes; this call takes {K}")
+    _fits(q, (N, K), "q")
+    if s.dim() > 1:
+        _fits(s, scales, "s")
     return p
 
 
@@ -436,9 +474,8 @@ def w4a8_quant_act_fp8(x, q, s, stream=None) -> None:
     dev = _device(x)
     _check("w4a8_quant_act_fp8",
            load_library().w4a8_quant_act_fp8(_ptr(x, dev), _dtype(x), M, K,
-                                             _typed(q, _CODES, dev, M * K, "q"),
-                                             _typed(s, _F32, dev, M * -(-K // 128) * 4, "s"),
-                                             _stream(stream)))
+                                             _typed_out(q, _CODES, M, K, dev, "q"),
+                                             _typed_out(s, _F32, M, -(-K // 128), dev, "s"), _stream(stream)))
 
 
 def w4a8_pack_fp8(w, q, s, stream=None) -> None:
@@ -446,9 +483,8 @@ def w4a8_pack_fp8(w, q, s, stream=None) -> None:
     N, K = w.shape
     dev = _device(w)
     _check("w4a8_pack_fp8",
-           load_library().w4a8_pack_fp8(_ptr(w, dev), _dtype(w), N, K,
-                                        _typed(q, _CODES, dev, N * K, "q"),
-                                        _typed(s, _F32, dev, _fp8_scales(N, K), "s"),
+           load_library().w4a8_pack_fp8(_ptr(w, dev), _dtype(w), N, K, _typed_out(q, _CODES, N, K, dev, "q"),
+                                        _typed_out(s, _F32, -(-N // 128), -(-K // 128), dev, "s"),
                                         _stream(stream)))
 
 
@@ -461,14 +497,12 @@ def w4a8_gemm_fp8(x, q, s, y, ws, bias=None, stream=None) -> None:
     M, K = x.shape
     N = q.shape[0]
     dev = _device(x)
-    codes = _codes(q, N, K, dev)
+    weight = _fp8_weight(q, s, N, K, dev)
     epi = _NO_BIAS.get(y.dtype) if bias is None else None
     if bias is not None or y.dtype not in _NO_BIAS:
         epi = ctypes.byref(_epilogue(bias, y, N, dev))
     _check("w4a8_gemm_fp8",
-           load_library().w4a8_gemm_fp8(M, N, K, _ptr(x, dev), _dtype(x), codes,
-                                        _typed(s, _F32, dev, _fp8_scales(N, K), "s"),
-                                        epi, _ptr(y, dev, M * N * y.element_size(), "y"),
+           load_library().w4a8_gemm_fp8(M, N, K, _ptr(x, dev), _dtype(x), *weight, epi, _out(y, M, N, dev, "y"),
                                         _ptr(ws, dev), ws.nbytes, _stream(stream)))
 
 
@@ -478,17 +512,20 @@ def w4a8_gemm_fp8_backward(dy, q, s, dx, ws, stream=None) -> None:
     K = dx.shape[1]
     dev = _device(dy)
     _check("w4a8_gemm_fp8_backward",
-           load_library().w4a8_gemm_fp8_backward(M, N, K, _ptr(dy, dev), _dtype(dy), _codes(q, N, K, dev),
-                                                 _typed(s, _F32, dev, _fp8_scales(N, K), "s"),
-                                                 _dtype(dx), _ptr(dx, dev, M * K * dx.element_size(), "dx"),
-                                                 _ptr(ws, dev), ws.nbytes, _stream(stream)))
+           load_library().w4a8_gemm_fp8_backward(M, N, K, _ptr(dy, dev), _dtype(dy), *_fp8_weight(q, s, N, K, dev),
+                                                 _dtype(dx), _out(dx, M, K, dev, "dx"), _ptr(ws, dev), ws.nbytes,
+                                                 _stream(stream)))
 
 
 def _router(wr: torch.Tensor, E: int, H: int, dev: int):
     p = _ptr(wr, dev, E * H * wr.element_size(), "wr")
-    if wr.shape != (E, H):
-        raise ValueError(f"libw4a8: wr is {tuple(wr.shape)}; this call takes ({E}, {H})")
+    _fits(wr, (E, H), "wr")
     return p
+
+
+def _slots(ids: torch.Tensor, weights: torch.Tensor, T: int, top_k: int, dev: int):
+    """Pointers of the slots' experts and weights, (T, top_k) each."""
+    return _typed_out(ids, _I32, T, top_k, dev, "ids"), _typed_out(weights, _F32, T, top_k, dev, "weights")
 
 
 def w4a8_moe_route(x, wr, top_k: int, ids, weights, renorm: bool = True, stream=None) -> None:
@@ -496,13 +533,10 @@ def w4a8_moe_route(x, wr, top_k: int, ids, weights, renorm: bool = True, stream=
     T, H = x.shape
     E = wr.shape[0]
     dev = _device(x)
-    n = T * top_k * 4
     _check("w4a8_moe_route",
            load_library().w4a8_moe_route(T, E, H, top_k, int(renorm), _ptr(x, dev), _dtype(x),
                                          _router(wr, E, H, dev), _dtype(wr),
-                                         _typed(ids, _I32, dev, n, "ids"),
-                                         _typed(weights, _F32, dev, n, "weights"),
-                                         _stream(stream)))
+                                         *_slots(ids, weights, T, top_k, dev), _stream(stream)))
 
 
 def w4a8_moe_workspace_bytes(T: int, E: int, H: int, I: int, top_k: int) -> int:
@@ -512,15 +546,19 @@ def w4a8_moe_workspace_bytes(T: int, E: int, H: int, I: int, top_k: int) -> int:
 def _experts(dev: int, H: int, gu_qs, gu_d, dn_qs, dn_d):
     """(E, I) and the pointers of stacked experts: gu_qs (E, 2I, H/2), gu_d (E, 2I, H/32),
     dn_qs (E, H, I/2), dn_d (E, H, I/32)."""
-    E, I = gu_qs.shape[0], gu_qs.shape[1] // 2
-    gq, gd = _q4_0_bytes(E * 2 * I, H)
-    dq, dd = _q4_0_bytes(E * H, I)
-    p = (_ptr(gu_qs, dev, gq, "gu_qs"), _ptr(gu_d, dev, gd, "gu_d"), _ptr(dn_qs, dev, dq, "dn_qs"),
-         _ptr(dn_d, dev, dd, "dn_d"))
-    if gu_qs.shape != (E, 2 * I, H // 2) or dn_qs.shape != (E, H, I // 2):
-        raise ValueError(f"libw4a8: experts of {tuple(gu_qs.shape)} and {tuple(dn_qs.shape)} codes; "
-                         f"this call takes (E, 2 I, {H} / 2) and (E, {H}, I / 2)")
-    return E, I, p
+    E, I2 = gu_qs.shape[0], gu_qs.shape[1] // 2 * 2
+    I, B = I2 // 2, H // 32
+    if not (gu_qs.shape == (E, I2, H // 2) and gu_d.shape == (E, I2, B) and dn_qs.shape == (E, H, I // 2)
+            and dn_d.shape == (E, H, I // 32) and gu_qs.element_size() == 1 == dn_qs.element_size()
+            and gu_d.element_size() == 2 == dn_d.element_size()):
+        for t, name, size, shape in ((gu_qs, "gu_qs", 1, (E, I2, H // 2)), (gu_d, "gu_d", 2, (E, I2, B)),
+                                     (dn_qs, "dn_qs", 1, (E, H, I // 2)), (dn_d, "dn_d", 2, (E, H, I // 32))):
+            _ptr(t, dev, math.prod(shape) * size, name)
+            _fits(t, shape, name)
+            if t.element_size() != size:
+                raise ValueError(f"libw4a8: {name} is {t.dtype}; this call takes elements of {size} bytes")
+    return E, I, (_ptr(gu_qs, dev, 0, "gu_qs"), _ptr(gu_d, dev, 0, "gu_d"), _ptr(dn_qs, dev, 0, "dn_qs"),
+                  _ptr(dn_d, dev, 0, "dn_d"))
 
 
 def w4a8_moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, y, ws, stream=None) -> None:
@@ -529,13 +567,10 @@ def w4a8_moe_q4_0(x, ids, weights, gu_qs, gu_d, dn_qs, dn_d, y, ws, stream=None)
     top_k = ids.shape[1]
     dev = _device(x)
     E, I, experts = _experts(dev, H, gu_qs, gu_d, dn_qs, dn_d)
-    n = T * top_k * 4
     _check("w4a8_moe_q4_0",
            load_library().w4a8_moe_q4_0(T, E, H, I, top_k, _ptr(x, dev), _dtype(x),
-                                        _typed(ids, _I32, dev, n, "ids"),
-                                        _typed(weights, _F32, dev, n, "weights"), *experts,
-                                        _dtype(y), _ptr(y, dev, T * H * y.element_size(), "y"), _ptr(ws, dev),
-                                        ws.nbytes, _stream(stream)))
+                                        *_slots(ids, weights, T, top_k, dev), *experts, _dtype(y),
+                                        _out(y, T, H, dev, "y"), _ptr(ws, dev), ws.nbytes, _stream(stream)))
 
 
 def w4a8_moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k: int, ids, weights, y, ws, renorm: bool = True,
@@ -544,14 +579,11 @@ def w4a8_moe_layer_q4_0(x, wr, gu_qs, gu_d, dn_qs, dn_d, top_k: int, ids, weight
     T, H = x.shape
     dev = _device(x)
     E, I, experts = _experts(dev, H, gu_qs, gu_d, dn_qs, dn_d)
-    n = T * top_k * 4
     _check("w4a8_moe_layer_q4_0",
            load_library().w4a8_moe_layer_q4_0(T, E, H, I, top_k, int(renorm), _ptr(x, dev), _dtype(x),
                                               _router(wr, E, H, dev), _dtype(wr), *experts,
-                                              _typed(ids, _I32, dev, n, "ids"),
-                                              _typed(weights, _F32, dev, n, "weights"),
-                                              _dtype(y), _ptr(y, dev, T * H * y.element_size(), "y"), _ptr(ws, dev),
-                                              ws.nbytes, _stream(stream)))
+                                              *_slots(ids, weights, T, top_k, dev), _dtype(y),
+                                              _out(y, T, H, dev, "y"), _ptr(ws, dev), ws.nbytes, _stream(stream)))
 
 
 def w4a8_last_device_error() -> int:

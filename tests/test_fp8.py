@@ -173,3 +173,25 @@ def test_binding_refuses_codes_of_another_width(fake, which):  # noqa: F811
     with pytest.raises(ValueError, match="rows of"):
         fn(**tensors)
     assert not fake.calls
+
+
+@pytest.mark.parametrize("which,key,shape", [
+    (0, "q", (272, 3)), (0, "s", (1, 9)), (1, "q", (272, 200)), (1, "s", (3, 2)), (2, "s", (3, 2)), (2, "s", (3, 3)),
+    (2, "y", (200, 3)), (2, "q", (200, 1, 272)), (3, "q", (201, 272)), (3, "q", (456, 272)), (3, "s", (3, 2))])
+def test_binding_refuses_tensors_laid_out_otherwise(fake, which, key, shape):  # noqa: F811
+    """The bytes are there, but in other rows; a gradient's weight of more rows than dy has columns is
+    another layer's."""
+    _, fn, tensors, _ = _tensors()[which]
+    tensors[key] = torch.zeros(*shape, dtype=torch.uint8).view(torch.float8_e4m3fn) if key == "q" else torch.zeros(*shape)
+    with pytest.raises(ValueError, match=f"libw4a8: {key} "):
+        fn(**tensors)
+    assert not fake.calls
+
+
+def test_binding_takes_larger_and_flat_outputs_and_flat_scales(fake):  # noqa: F811
+    _, fn, tensors, _ = _tensors()[2]
+    fn(**{**tensors, "y": torch.zeros(64, 200), "s": torch.zeros(6)})
+    fn(**{**tensors, "y": torch.zeros(600)})
+    _, fn, tensors, _ = _tensors()[0]
+    fn(**{**tensors, "q": torch.zeros(9, 272, dtype=torch.uint8), "s": torch.zeros(9, 3)})
+    assert len(fake.calls) == 3

@@ -214,3 +214,25 @@ def test_binding_refuses_tensors_that_do_not_fit_together(fake, change):  # noqa
     with pytest.raises(ValueError):
         fn(**tensors, **other)
     assert not fake.calls
+
+
+@pytest.mark.parametrize("which,key,bad", [
+    (0, "ids", torch.zeros(2, 3, dtype=torch.int32)), (0, "weights", torch.zeros(2, 3)),
+    (1, "weights", torch.zeros(2, 3)), (1, "gu_qs", torch.zeros(4, 192, 32, dtype=torch.int32)),
+    (1, "gu_d", torch.zeros(4, 2, 192, dtype=torch.int16)), (1, "gu_d", torch.zeros(4, 192, 2)),
+    (1, "gu_d", torch.zeros(8, 192, 2, dtype=torch.int16)), (1, "dn_d", torch.zeros(4, 3, 64, dtype=torch.int16)),
+    (1, "dn_d", torch.zeros(4, 64, 3)), (1, "dn_qs", torch.zeros(4, 64, 48, dtype=torch.int16)),
+    (1, "y", torch.zeros(64, 3)), (2, "ids", torch.zeros(2, 3, dtype=torch.int32)), (2, "y", torch.zeros(64, 3))],
+    ids=lambda v: str(tuple(v.shape)) if isinstance(v, torch.Tensor) else str(v))
+def test_binding_refuses_tensors_laid_out_otherwise(fake, which, key, bad):  # noqa: F811
+    """The bytes are there, but in other rows, as turned round, or of another element type."""
+    _, fn, tensors, other, _ = _tensors()[which]
+    with pytest.raises(ValueError, match=f"libw4a8: {key} "):
+        fn(**{**tensors, key: bad}, **other)
+    assert not fake.calls
+
+
+def test_binding_takes_larger_and_flat_outputs(fake):  # noqa: F811
+    _, fn, tensors, other, _ = _tensors()[2]
+    fn(**{**tensors, "y": torch.zeros(9, 64), "ids": torch.zeros(9, 2, dtype=torch.int32), "weights": torch.zeros(6)}, **other)
+    assert len(fake.calls) == 1
