@@ -338,6 +338,9 @@ w4a8_status w4a8_pack_fp8(const void* w, w4a8_dtype dtype, int N, int K, uint8_t
  * block, then one rounding per block and per CTA that shares the axis). Every output is
  * within 1e-5 * sum |terms| of the exact sum over the codes for contracted axes up to 16384,
  * and within (length / 128 + 40) * 2^-24 * sum |terms| beyond (plus the rounding to bf16). The
+ * two scales of a block are multiplied in f32: where their product lies below 2^-126 (rows of x
+ * around 1e-34 on weights around 0.01) it is held in steps of 2^-149, which adds up to
+ * 2^-150 * sum |qx * q| and 2^-150 per block; a product beyond the f32 range is infinite. The
  * result does not depend on scheduling.
  * Few rows of x run tiles of 128 columns by 16 to 64 rows, the contracted axis split over a
  * cluster; a handful (M <= 16 with few blocks per CTA) are quantised inside that kernel, and
@@ -383,7 +386,8 @@ w4a8_status w4a8_gemm_fp8_backward(int M, int N, int K, const void* dy, w4a8_dty
  * w4a8_gemm (no f32 chain is longer than 128 blocks), and within (150 + width / 4096) * 2^-24 *
  * sum |block terms| beyond; the sum over a token's slots adds at most I / 4096 + 2 roundings of f32 per slot.
  * A value of h so close to a rounding border that this error carries it across changes by one
- * step of its block. A call's result does not depend on scheduling; the order of a token's sum over
+ * step of its block. A block of h whose largest value is below about 1e-33 is held less exactly (its
+ * scale times a weight's is subnormal). A call's result does not depend on scheduling; the order of a token's sum over
  * experts may depend on which other experts the batch uses.
  * Limits: T <= W4A8_MOE_MAX_TOKENS (the routed calls), E <= W4A8_MOE_MAX_EXPERTS, top_k <=
  * min(E, W4A8_MOE_MAX_TOPK), I <= W4A8_MAX_DIM / 2; H and I multiples of 32.

@@ -179,6 +179,23 @@ def test_long_sums_of_one_sign(M, N, K):
         assert float(((dx - want).abs() / want).max()) <= TOL
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 130, 512), (20, 257, 2048), (300, 384, 400), (2600, 1030, 272)])
+@pytest.mark.parametrize("size", [1e-31, 1e-34, 1e-36, 1e-38])
+def test_scales_whose_product_is_subnormal(M, N, K, size):
+    """Rows so small that a block's two scales multiply to less than 2^-126: the product is off by up
+    to 2^-150, times the codes' products, and so is each block's f32 sum."""
+    w = rand((N, K), 7, spread=0.5) * 0.01
+    q, s = w4a8.pack_fp8(w.cuda())
+    wq, ws = ref.decode(q.view(torch.uint8).cpu().numpy()), s.cpu().numpy()
+    x, dy = rand((M, K), M) * size, rand((M, N), M + 1) * size
+    for inp, call, plain, side in ((x, w4a8.gemm_fp8, ref.gemm, np.abs(wq).T), (dy, w4a8.gemm_fp8_backward, ref.backward, np.abs(wq))):
+        y = call(inp.cuda(), q, s).cpu().numpy().astype(np.float64)
+        yref, T = plain(inp.numpy(), wq, ws)
+        codes = np.abs(ref.quant_rows(inp.numpy())[0]) @ side
+        blocks = -(-inp.shape[1] // 128)
+        assert np.all(np.abs(y - yref) <= TOL * T + 2.0 ** -150 * (codes + blocks + 1))
+
+
 # ------------------------------------------------------------------ memory, streams, graphs
 @pytest.mark.parametrize("M,N,K", [(1, 1000, 1040), (16, 129, 144), (70, 333, 400), (201, 1531, 1936),
                                    (1100, 2090, 2064)])
