@@ -109,6 +109,32 @@ def test_wide_outputs_with_a_bias(M, N, K, bias_dtype, dtype):
     assert w4a8.w4a8_last_device_error() == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 19001, 1024), (1, 32000, 2048), (3, 19072, 1040), (16, 19072, 1040), (20, 19001, 784),
+                                   (40, 19072, 1040), (64, 20000, 400)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_wide_outputs_of_few_tokens(M, N, K, dtype):
+    """More than 148 column tiles for at most 64 tokens: one CTA walks all blocks of its tile and stores
+    without a join, with a bias, in whole 16-byte rows or not; quantised inside or before."""
+    q, s, wq, ws = weights(N, K, N + K)
+    x = rand((M, K), M, dtype)
+    bias = torch.randn(N, generator=torch.Generator().manual_seed(1))
+    for b in (None, bias):
+        y = w4a8.gemm_fp8(x.cuda(), q, s, bias=None if b is None else b.cuda(), out_dtype=dtype)
+        yref, T = ref.gemm(x.float().numpy(), wq, ws, None if b is None else b.numpy().astype(np.float64))
+        check(y, yref, T, f"{M}x{N}x{K}")
+    assert w4a8.w4a8_last_device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 19008), (16, 1040, 19008), (33, 777, 20000)])
+def test_wide_gradients_of_few_tokens(M, N, K):
+    q, s, wq, ws = weights(N, K, N + K + 1)
+    dy = rand((M, N), M + 1)
+    dx = w4a8.gemm_fp8_backward(dy.cuda(), q, s)
+    dref, T = ref.backward(dy.numpy(), wq, ws)
+    check(dx, dref, T, f"{M}x{N}x{K}")
+    assert w4a8.w4a8_last_device_error() == 0
+
+
 def test_backward_agrees_with_differences_of_the_forward():
     """With x and dy on the e4m3 grid (scale 1 in every block, so neither call rounds its
     input), <dy, y(x + e) - y(x - e)> = <dx, 2e> up to the f32 sums of both calls."""

@@ -97,6 +97,13 @@ def test_scale_rows_with_and_without_a_tensor_map(T, H, I):
     verify(*make(T, 4, H, I, 2, H + 2 * I + T), torch.float32, TOL)
 
 
+@pytest.mark.parametrize("T,E,H,I,k", [(33, 2, 4096, 64, 1), (64, 3, 2432, 288, 2), (1, 2, 4768, 96, 2), (40, 2, 2048, 512, 1),
+                                       (5, 2, 1216, 96, 1), (2, 2, 2368, 320, 2)])
+def test_every_cluster_size_of_down(T, E, H, I, k):
+    """CTAs per 32 rows of H on 148 SMs: 1 (the first three), 2, 4, 4; smaller layers take 8."""
+    verify(*make(T, E, H, I, k, T + H + I), torch.float32, TOL)
+
+
 def test_empty_slots_repeated_experts_and_empty_tokens():
     T, E, H, I, k = 6, 5, 256, 96, 3
     x, gu, dn, ids, weights = make(T, E, H, I, k, 3)
