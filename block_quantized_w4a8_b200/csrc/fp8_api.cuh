@@ -67,10 +67,12 @@ inline bool fp8_dims_ok(int M, int N, int K) { return dims_ok(M, N) && dims_ok(K
 // 24.8 / 19.2; K = 1024: 300 x 4096 (160) 10.9 / 12.6; K = 8192: 512 x 2048 (128) 38.4 / 27.9.
 inline bool fp8_use_pair(int M, int C) { return M > 64 && cdiv(M, 64) * cdiv(C, 128) > sm_count(); }
 
-// Split of the contracted axis for the few-token kernel: the largest power of two (other
-// cluster sizes leave SMs of a GPC unused) whose CTAs are all resident, two per SM. Tiles of
-// 64 tokens stop at 4, since every CTA's partial sums are read by the others (64 tokens at 4096 x 4096:
-// 4 CTAs per tile 9.6 us, 8 CTAs 11.0; one token: 8 CTAs 6.9, 4 CTAs 7.5).
+// Split of the contracted axis for the few-token kernel: the largest power of two whose CTAs are
+// all resident, two per SM, sets the blocks per CTA, and CTAs that would have none are not launched, so
+// that the cluster may be of any size up to 8 (one token of 4096 columns, 9, 13, 17 and 33 blocks: 5, 7, 6 and
+// 7 CTAs take 5.2, 5.4, 5.4 and 6.5 us; the next smaller splits of 3 and 4 CTAs 5.4, 5.5, 5.9 and 7.1).
+// Tiles of 64 tokens stop at 4, since every CTA's partial sums are read by the others (64 tokens at
+// 4096 x 4096: 4 CTAs per tile 9.6 us, 8 CTAs 11.0; one token: 8 CTAs 6.3, 4 CTAs 6.8).
 struct Fp8Split {
     int ks, kbs;  // CTAs per output tile, blocks per CTA
 };

@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(RowsGeo<MN, FUSE>::THREADS, 2)
     } else {
         const uint32_t lane_base = tmem_base + (uint32_t(warp * 32) << 16);
         if constexpr (FUSE) {
-            // 16 lanes per token and block, as quant_rows_kernel; codes into the operand's layout
-            // (rows of 128 bytes, 128-byte swizzle). Rows past M keep what the memory held: they
+            // 16 lanes of 8 elements per token and block, the arithmetic of quant_rows_kernel; codes into
+            // the operand's layout (rows of 128 bytes, 128-byte swizzle). Rows past M keep what the memory held: they
             // only reach columns that are not stored.
             pdl_wait_primary();
             const int sub = lane & 15, tokens = min(MN, M - m0), n = tokens * Bl;
@@ -422,8 +422,8 @@ struct PairCtrl {
 };
 static_assert(sizeof(PairCtrl) <= 512, "control block");
 
-// Tile order: token tiles fastest within bands of 16 column tiles, so that the CTAs running
-// at one time share weights and tokens in L2.
+// Tile order: column tiles fastest within bands of 16 of them, then token tiles, so that the CTAs
+// running at one time share weights and tokens in L2.
 __device__ __forceinline__ void pair_tile(int t, int tm, int tc, int& mt, int& ct) {
     constexpr int BAND = 16;
     const int band = t / (tm * BAND), in = t - band * tm * BAND;

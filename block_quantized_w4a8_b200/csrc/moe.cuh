@@ -84,7 +84,7 @@ constexpr int kShallowTokens = 8;
 // Grid: kRouteCtas CTAs (a cluster) per token. Every CTA quantises its share of the token's
 // blocks (xq != nullptr) and, with ROUTE, computes the logits of its experts, a warp each;
 // they meet in the first CTA's shared memory, where one warp takes the top_k. Bound by latency,
-// not bytes: about a tenth of the 107 us of a layer of 64 tokens and 64 experts of 2048 x 1024.
+// not bytes: about a tenth of the 106 us of a layer of 64 tokens and 64 experts of 2048 x 1024.
 // DEEP: steps of 256 columns whose loads are in flight together per warp.
 template <bool ROUTE, bool XB, bool WB, int DEEP>
 __global__ void __launch_bounds__(256, 1) route_kernel(int E, int H, int top_k, int renorm, const void* __restrict__ x,
@@ -605,9 +605,9 @@ __host__ __device__ __forceinline__ size_t gate_up_smem(int E, int n) {
 // sums meet in shared memory, where a warp per token and 32 rows forms h, its block's scale
 // and codes. RG = 2 spreads few items over the GPU; RG = 4 (I a multiple of 64) halves what an
 // item costs beside its boxes. Two CTAs per SM. 64 tokens, top 8 of 64 experts of 2048 x 1024:
-// 66 us for 151 MB, bound by instruction issue (32 M warp instructions, 0.52 per cycle and
-// scheduler); 4 tokens, top 2 of 8 experts of 4096 x 14336: 122 us for the whole layer, two
-// thirds of the copy rate, the rest uneven rounds of items.
+// 65 us for 151 MB, bound by instruction issue (32 M warp instructions, 0.53 per cycle and
+// scheduler); 4 tokens, top 2 of 8 experts of 4096 x 14336: 118 to 121 us for the whole layer, about
+// two thirds of the copy rate, the rest uneven rounds of items.
 template <int RG>
 __global__ void __launch_bounds__(256, 2)
     gate_up_kernel(int T, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* xq,
@@ -746,7 +746,7 @@ __host__ __device__ __forceinline__ size_t down_smem(int T, int E, int n) {
 // for those rows are dealt in runs to the warps of the cluster; each warp adds its sums,
 // times the slots' weights, to a [token][row] array of its own, and the arrays are added in a
 // fixed order (within the CTA, then across the cluster through distributed shared memory).
-// 64 tokens, top 8 of 64 experts of 2048 x 1024: 51 us for 75 MB, bound by instruction issue.
+// 64 tokens, top 8 of 64 experts of 2048 x 1024: 50 us for 75 MB, bound by instruction issue.
 __global__ void __launch_bounds__(256, 2)
     down_kernel(int Tall, int E, int H, int I, int top_k, const int* ids, const float* weights, const uint8_t* hq,
                 const float* hd, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_s,

@@ -345,6 +345,9 @@ w4a8_status w4a8_pack_fp8(const void* w, w4a8_dtype dtype, int N, int K, uint8_t
  * Few rows of x run tiles of 128 columns by 16 to 64 rows, the contracted axis split over a
  * cluster; a handful (M <= 16 with few blocks per CTA) are quantised inside that kernel, and
  * the workspace is then only checked; more such tiles of 64 rows than SMs run on CTA pairs.
+ * Weights (here and in the expert layer) may be read before the preceding kernel of the stream has
+ * completed if that one lets its successor start early (programmatic dependent launch), as no
+ * kernel of this library that writes weights does.
  * ws : w4a8_fp8_workspace_bytes(M, N, K) bytes (serves both calls; query it with the device
  *      current), 16-byte aligned; contents ignored on entry, garbage afterwards. Calls that
  *      share a workspace must be ordered on one stream. Returns 0 for invalid sizes.
