@@ -104,7 +104,7 @@ constexpr int kMaxSplit = 8;  // CTAs that share the contracted axis (a portable
 // FUSE (a handful of token blocks per CTA): the CTA quantises its share of the activation
 // itself, while the first weight tiles arrive, and no other kernel runs. The weights' bytes are the
 // bound: 16 x 14336 x 4096 takes 16.2 us with the quantisation (58.7 MB at 3.6 TB/s; 224 CTAs leave
-// half of the SMs with one), one token at 4096 x 4096 6.4 us, mostly the latency of a launch, the first
+// half of the SMs with one), one token at 4096 x 4096 6.3 us, mostly the latency of a launch, the first
 // tiles and the join. mma.sync would need the codes widened in registers; tcgen05 reads them as they lie.
 template <int MN_, bool FUSE>
 struct RowsGeo {
@@ -317,12 +317,21 @@ __global__ void __launch_bounds__(RowsGeo<MN, FUSE>::THREADS, 2)
         }
     }
 
+    // The tensor memory goes back before the CTA waits for its cluster: one that held columns while it
+    // waited for a CTA that still waits for columns of another kernel (whose own CTAs may need these)
+    // could close a circle.
+    tc_fence_before();
+    __syncthreads();
+    if (warp == G::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, G::COLS);
+    }
+
     const int ks = gridDim.x;
     const int tokens = min(MN, M - m0);
     if (ks > 1) {
         // partial sums [token][128] over the stages, which every MMA has finished reading
         float* red = reinterpret_cast<float*>(smem);
-        __syncthreads();
         if (warp < G::EPI_WARPS) {
 #pragma unroll
             for (int j = 0; j < CW; ++j) red[j * 128 + warp * 32 + lane] = acc[j];
@@ -370,12 +379,6 @@ __global__ void __launch_bounds__(RowsGeo<MN, FUSE>::THREADS, 2)
             for (int j = 0; j < CW; ++j)
                 if (j < tokens) epi_store(out, int64_t(m0 + j) * C + c, c, acc[j], epi);
         }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == G::MMA_WARP) {
-        tc_fence_after();
-        tmem_dealloc(tmem_base, G::COLS);
     }
 }
 

@@ -276,6 +276,27 @@ def test_side_streams_and_captured_graphs(M, N, K):
     assert torch.equal(y, w4a8.gemm_fp8(x, q, s))
 
 
+def test_beside_the_other_tensor_core_kernels():
+    """Few-token tiles and CTA pairs in FP8 next to the int8 and fp16 kernels on four streams, all of which
+    share the SMs' tensor memory: each gives what it gives alone."""
+    N, K = 1024, 2048
+    q, s, _, _ = weights(N, K, 27)
+    qs, d = w4a8.pack_q4_0(rand((N, K), 28).cuda())
+    jobs = [lambda x=rand((M, K), M).cuda(): w4a8.gemm_fp8(x, q, s) for M in (1, 64, 200, 2500)]
+    jobs += [lambda x=rand((M, K), M + 1).cuda(): w4a8.gemm(x, qs, d) for M in (16, 64, 300)]
+    want = [job() for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for i in range(40):
+        for j, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append(((i + 2 * j) % len(jobs), jobs[(i + 2 * j) % len(jobs)]()))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[k]) for k, y in got)
+    assert w4a8.w4a8_last_device_error() == 0
+
+
 def test_helpers_on_a_stream_argument_keep_their_memory():
     """Outputs and workspace of a call on another stream are not handed out again while it waits
     there: the current stream allocates and fills memory of the same sizes meanwhile."""
