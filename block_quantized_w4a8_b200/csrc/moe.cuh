@@ -800,9 +800,7 @@ __global__ void __launch_bounds__(256, 2)
     pdl_wait_primary();  // hq and hd
 
     float* yw = ybuf + warp * YT;
-    Sums acc;
-    Group gr;
-    auto flush = [&]() {
+    auto flush = [&](const Group& gr, const Sums& acc) {
         if (gr.cnt == 1) {
             const int entry = l.ord[gr.first];
             float* p = yw + (entry >> 10) * kYPitch + lane;
@@ -829,10 +827,12 @@ __global__ void __launch_bounds__(256, 2)
     while (left > 0) {  // the run's part in one group, at most kChainBoxes boxes at a time
         const int end = min(uj + min(left, kChainBoxes), nbox);
         left -= end - uj;
+        Group gr;
         gr.template set<false>(l, ug);
         const uint8_t* xb = hq + int64_t(gr.b) * pitch;
         const float *d0 = hd + int64_t(gr.s0) * Bp, *d1 = hd + int64_t(gr.s1) * Bp;
         const int r = int(l.act[ug]) * H + n0;
+        Sums acc;
         acc.clear();
 #pragma unroll 1
         for (; uj < end; ++uj) {
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(256, 2)
             ++ring.used;
             fetch();
         }
-        flush();
+        flush(gr, acc);
         if (uj == nbox) {
             uj = 0;
             ++ug;
